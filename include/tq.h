@@ -68,6 +68,8 @@ typedef enum {
 #define TQ_DEVERR_POS_RANGE 0x4u   /* tq_attend_decode: a position > s_max was clamped */
 #define TQ_DEVERR_SMEM_LAYOUT 0x8u /* tq_attend_decode: shared memory not where the launch planned it; no output */
 #define TQ_DEVERR_BLOCK_RANGE 0x10u /* tq_attend_decode_paged: a block number outside [0, num_blocks) was clamped */
+#define TQ_DEVERR_ROW_RANGE 0x20u   /* tq_attend_window: offsets out of range; tq_pages_fork: a row out of range or named twice */
+#define TQ_DEVERR_POOL_FULL 0x40u   /* tq_pages_fork: no free page left for a child's last page */
 
 /* Human-readable name of a status. Never NULL. */
 const char* tq_status_string(tq_status s);
@@ -320,6 +322,176 @@ tq_status tq_attend_decode_static(const tq_ctx* k, const tq_ctx* v, const void* 
                                   const void* k_packed, const float* k_norms, const void* v_packed,
                                   const float* v_norms, int64_t s_max, const int32_t* positions, void* out_f16,
                                   tq_stream stream);
+
+/* Element types of tq_qk_norm_rope's inputs. */
+#define TQ_F16 0
+#define TQ_BF16 1
+
+/*
+ * Norm of every query and key head and rotation by position, in one pass (an
+ * addition of this library: the step between a layer's projection and
+ * tq_encode_slots / the attention calls, whose keys and queries carry their
+ * positions). For a token at position p and a head row x:
+ *   y = x / sqrt(mean(x^2) + eps) * weight     (y = x where the weight is NULL)
+ *   (y_a, y_b) <- rope_scale * (y_a cos(p f_i) - y_b sin(p f_i),
+ *                               y_b cos(p f_i) + y_a sin(p f_i)),  i < rot_dim / 2
+ * with (a, b) = (2 i, 2 i + 1) if `interleaved`, else (i, i + rot_dim / 2);
+ * coordinates from rot_dim on are not rotated (nor scaled). Computed in f32
+ * with the angle reduced in f64, rounded once to fp16.
+ *   q, k        device, n_tok x hq (hkv) rows of head_dim elements of `dtype`,
+ *               row (t, h) at element t * tok_stride + h * head_stride; 16-byte
+ *               aligned, strides multiples of 8 (views of one projection's
+ *               output are fine).
+ *   positions   device, [n_tok] int32 (any value).
+ *   inv_freq    device, [rot_dim / 2] float64: f_i, radians per position. NULL
+ *               with rot_dim 0 (norm only).
+ *   rot_dim     even, 0 ... head_dim.
+ *   q_weight, k_weight  device, [head_dim], 16-byte aligned, of `dtype`, or
+ *               float32 if weight_f32; NULL: no norm.
+ *   eps         >= 0 (a zero row with eps 0 gives NaN).
+ *   q_out, k_out device, [n_tok, hq (hkv), head_dim] fp16, dense, 16-byte
+ *               aligned. Each may be its own input where that is dense fp16;
+ *               otherwise outputs and inputs must not overlap.
+ * head_dim as tq_create's. n_tok == 0 is a no-op. Asynchronous on `stream`.
+ */
+tq_status tq_qk_norm_rope(const void* q, const void* k, int dtype, int64_t n_tok, int hq, int hkv, int head_dim,
+                          int64_t q_tok_stride, int64_t q_head_stride, int64_t k_tok_stride, int64_t k_head_stride,
+                          const int32_t* positions, const double* inv_freq, int rot_dim, int interleaved,
+                          float rope_scale, const void* q_weight, const void* k_weight, int weight_f32, float eps,
+                          void* q_out, void* k_out, tq_stream stream);
+
+/*
+ * Workspace (device bytes) of tq_attend_window and tq_attend_window_paged
+ * (s_max = max_blocks * 16) for these sizes; 0 if none is needed or the sizes
+ * are invalid.
+ */
+size_t tq_attend_window_workspace_bytes(int64_t n_tok, int B, int max_q, int hq, int hkv, int head_dim, int64_t s_max,
+                                        int64_t window, int64_t sinks);
+
+/*
+ * Attention of one or more query tokens per sequence over packed caches,
+ * causal, within a sliding window and the first positions (an addition of
+ * this library, beside tq_attend_decode: a serving engine also verifies
+ * drafted tokens and continues prompts in chunks over the cache, and bounds
+ * long contexts by a window whose first `sinks` tokens stay visible). The
+ * keys and values of the query tokens themselves have been encoded into the
+ * cache already. Query token i of a sequence with n query tokens and context
+ * length L stands at position p = L - n + i and sees the positions t with
+ *   t <= p  and  (t < sinks  or  t > p - window);
+ * a token that sees nothing (p < 0) gets a zero row.
+ *   q_f16       device, [n_tok, hq, d] fp16, 16-byte aligned; the sequences'
+ *               query tokens one after another.
+ *   q_offsets   device, [B + 1] int32: sequence b's tokens are
+ *               [q_offsets[b], q_offsets[b + 1]), at most max_q of them (none
+ *               is fine). NULL: one token per sequence (n_tok == B, max_q 1).
+ *               A sequence whose offsets leave [0, n_tok], decrease or exceed
+ *               max_q is left out and flagged with TQ_DEVERR_ROW_RANGE. Rows
+ *               of tokens in no sequence are not written.
+ *   context_lens device, [B] int32: L, the query tokens included. <= 0 gives
+ *               zero rows; > s_max is clamped and flagged with
+ *               TQ_DEVERR_POS_RANGE.
+ *   window      >= 1, or <= 0 for no limit.   sinks: >= 0.
+ *   k_cache ... as tq_attend_decode: [B, s_max, hkv, P] and norms
+ *               [B, s_max, hkv]; positions that no query sees are not read.
+ *   out_f16     device, [n_tok, hq, d] fp16 out, 16-byte aligned.
+ *   workspace   at least tq_attend_window_workspace_bytes(...) bytes, 16-byte
+ *               aligned (NULL if that is 0); contents on entry do not matter.
+ * Any hq that is a multiple of hkv. s_max below 2^31 - 256, B at most 65535.
+ * Asynchronous on `stream`; calls that share a workspace must not overlap.
+ */
+tq_status tq_attend_window(const tq_ctx* k, const tq_ctx* v, const void* q_f16, int64_t n_tok, int B,
+                           const int32_t* q_offsets, int max_q, int hq, int hkv, const void* k_cache,
+                           const float* k_norms, const void* v_cache, const float* v_norms, int64_t s_max,
+                           const int32_t* context_lens, int64_t window, int64_t sinks, void* out_f16,
+                           void* workspace, size_t ws_bytes, tq_stream stream);
+
+/*
+ * tq_attend_window over a paged cache (the pools and block tables of
+ * tq_attend_decode_paged). Table entries of pages that no query sees are not
+ * read (tq_pages_trim sets them to -1); one that is read and lies outside
+ * [0, num_blocks) is clamped and flagged with TQ_DEVERR_BLOCK_RANGE.
+ */
+tq_status tq_attend_window_paged(const tq_ctx* k, const tq_ctx* v, const void* q_f16, int64_t n_tok, int B,
+                                 const int32_t* q_offsets, int max_q, int hq, int hkv, const void* k_cache,
+                                 const float* k_norms, const void* v_cache, const float* v_norms,
+                                 int64_t num_blocks, const int32_t* block_tables, int max_blocks,
+                                 const int32_t* context_lens, int64_t window, int64_t sinks, void* out_f16,
+                                 void* workspace, size_t ws_bytes, tq_stream stream);
+
+/*
+ * Pages of a paged cache (an addition of this library: the page operations
+ * that a serving engine needs beside tq_encode_slots and the paged attention
+ * calls). The state is on the device:
+ *   block_tables [n_rows, max_blocks] int32, as tq_attend_decode_paged's, one
+ *                row per sequence slot; negative entries hold no page;
+ *   lens         [n_rows] int32: positions in use of each row;
+ *   refs         [num_blocks] int32: how many rows list each page (<= 0: the
+ *                page is free). The caller keeps it in line with the tables.
+ * Every call reads one set of arrays and writes another; each output may be
+ * its own input (in place), and must not overlap anything else. A table entry
+ * at or above num_blocks that is met is dropped (-1) and flagged with
+ * TQ_DEVERR_BLOCK_RANGE; a length above max_blocks * 16 counts as that and is
+ * flagged with TQ_DEVERR_POS_RANGE. All calls are asynchronous on `stream`,
+ * need no host synchronisation and can be captured into a graph.
+ *
+ * A pool is an array of num_blocks pages of block_bytes each (codes or norms
+ * of one layer): base 16-byte aligned, block_bytes a positive multiple of 16
+ * below 2^31; at most TQ_MAX_PAGE_POOLS of them per call.
+ */
+#define TQ_MAX_PAGE_POOLS 512
+#define TQ_MAX_PAGE_ROWS 131072
+typedef struct {
+  void* base;
+  int64_t block_bytes;
+} tq_page_pool;
+
+/*
+ * Fork n sequences: row children[i] becomes a copy of row parents[i]. The
+ * pages that the parent has filled are shared (refs + 1); its last page, if
+ * partly filled, is copied in every pool to the lowest free page (the forks
+ * take free pages in list order, refs becomes 1). The child's other entries
+ * become -1. A child row's former pages are not released: give it back with
+ * tq_pages_trim first.
+ * A fork whose rows lie outside the table, whose child is named twice or
+ * whose child is also a parent in the list is skipped and flagged with
+ * TQ_DEVERR_ROW_RANGE. Where no free page is left the child gets length 0 and
+ * no pages, flagged with TQ_DEVERR_POOL_FULL.
+ *   workspace   tq_pages_fork_workspace_bytes(n) bytes, 16-byte aligned.
+ * n <= n_rows <= TQ_MAX_PAGE_ROWS.
+ */
+size_t tq_pages_fork_workspace_bytes(int n);
+tq_status tq_pages_fork(const tq_page_pool* pools, int n_pools, int64_t num_blocks, const int32_t* block_tables,
+                        int32_t* tables_out, const int32_t* lens, int32_t* lens_out, const int32_t* refs,
+                        int32_t* refs_out, int n_rows, int max_blocks, const int32_t* parents,
+                        const int32_t* children, int n, void* workspace, size_t ws_bytes, tq_stream stream);
+
+/*
+ * Give pages back: of rows with release[row] != 0 all of them (the length
+ * becomes 0), of the others those that no query of tq_attend_window_paged
+ * with this window and sinks sees from the row's last token on: pages that
+ * hold no position below `sinks` and end at or before lens - window. Their
+ * entries become -1 and their refs go down by one.
+ *   window      >= 0, or < 0 for no window (rows are only released).
+ *   release     device, [n_rows] uint8, or NULL.
+ */
+tq_status tq_pages_trim(const int32_t* block_tables, int32_t* tables_out, const int32_t* lens, int32_t* lens_out,
+                        const int32_t* refs, int32_t* refs_out, int n_rows, int max_blocks, int64_t num_blocks,
+                        int64_t window, int64_t sinks, const uint8_t* release, tq_stream stream);
+
+/*
+ * Move the used pages to the front: with U used pages (refs > 0), the k-th
+ * used page at or above U moves, in every pool, to the k-th free page below
+ * U; table entries and refs follow. Entries of free pages become -1.
+ *   remap       device, [num_blocks] int32 out: the new number of every page,
+ *               -1 for free ones (for tables kept elsewhere).
+ *   used        device, [1] int32 out: U; every page from U on is free.
+ *   workspace   tq_pages_compact_workspace_bytes(num_blocks) bytes, 16-byte
+ *               aligned.
+ */
+size_t tq_pages_compact_workspace_bytes(int64_t num_blocks);
+tq_status tq_pages_compact(const tq_page_pool* pools, int n_pools, int64_t num_blocks, const int32_t* block_tables,
+                           int32_t* tables_out, const int32_t* refs, int32_t* refs_out, int n_rows, int max_blocks,
+                           int32_t* remap, int32_t* used, void* workspace, size_t ws_bytes, tq_stream stream);
 
 /*
  * Check, on the current device, the tensor-core arithmetic that the bulk

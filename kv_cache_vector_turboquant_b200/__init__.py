@@ -10,10 +10,15 @@ TurboQuant", "API Reference": ``TurboQuant(head_dim, bits, seed=42)``,
 
 from __future__ import annotations
 
+import contextlib
+
 from ._binding import (  # noqa: F401
     LIB_PATH,
+    TQ_BF16,
     TQ_DEVERR_BLOCK_RANGE,
+    TQ_DEVERR_POOL_FULL,
     TQ_DEVERR_POS_RANGE,
+    TQ_DEVERR_ROW_RANGE,
     TQ_DEVERR_SLOT_RANGE,
     TQ_DEVERR_SMEM_LAYOUT,
     TQ_DEVERR_TIMEOUT,
@@ -25,14 +30,21 @@ from ._binding import (  # noqa: F401
     TQ_ERR_TIMEOUT,
     TQ_ERR_UNSUPPORTED,
     TQ_ERR_WORKSPACE,
+    TQ_F16,
+    TQ_MAX_PAGE_POOLS,
+    TQ_MAX_PAGE_ROWS,
     TQ_OK,
     TQ_PAGE_BLOCK,
     Ctx,
+    PagePool,
     TQError,
     TQ_ATTEND_STATIC_SCRATCH_BYTES,
     tq_attend_decode,
     tq_attend_decode_paged,
     tq_attend_decode_static,
+    tq_attend_window,
+    tq_attend_window_paged,
+    tq_attend_window_workspace_bytes,
     tq_attend_workspace_bytes,
     tq_create,
     tq_decode,
@@ -45,6 +57,12 @@ from ._binding import (  # noqa: F401
     tq_decode_os,
     tq_encode_slots,
     tq_get_tables,
+    tq_pages_compact,
+    tq_pages_compact_workspace_bytes,
+    tq_pages_fork,
+    tq_pages_fork_workspace_bytes,
+    tq_pages_trim,
+    tq_qk_norm_rope,
     tq_status_string,
     tq_tensor_core_check,
 )
@@ -75,6 +93,33 @@ def _on_device(**tensors) -> None:
     here, before a pointer reaches the library."""
     for name, t in tensors.items():
         _require(t.is_cuda, f"{name}: a CUDA tensor")
+
+
+@contextlib.contextmanager
+def _launching(device, stream):
+    """Make `device` current and, where a stream is given, that stream: what
+    is allocated inside then belongs to the stream that uses it."""
+    import torch
+
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            _require(stream.device == device, f"stream: one of {device}, got {stream.device}")
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _one_device(tensors) -> "torch.device":
+    """The CUDA device that holds all the (name, tensor) pairs."""
+    first = None
+    for name, t in tensors:
+        _require(t.is_cuda, f"{name}: a CUDA tensor")
+        first = t.device if first is None else first
+        _require(t.device == first, f"{name}: on {first} like the other tensors, got {t.device}")
+    return first
 
 
 class TurboQuant:
@@ -314,6 +359,28 @@ class TQPagedAttention:
 
     __call__ = forward
 
+    def step(self, query, key, value, positions, slot_mapping, k_packed, k_norms, v_packed, v_norms, block_tables,
+             context_lens, window=None, sinks=0, q_offsets=None, max_q=None, inv_freq=None, interleaved=False,
+             rope_scale=1.0, q_weight=None, k_weight=None, eps=1e-6, stream=None):
+        """One layer's attention for the new tokens of a batch, from their
+        projections on: `qk_norm_rope` of query [T, num_query_heads, d] and
+        key [T, Hkv, d] at `positions` [T], `encode_slots` of keys and values
+        [T, Hkv, d] fp16 to slot_mapping [T] of the pools, then
+        `attend_window_paged`. The tables and context_lens include the new
+        tokens. Returns [T, num_query_heads, d] fp16."""
+        _require(query.dim() == 3 and query.shape[1] == self.num_query_heads,
+                 "query must be [T, num_query_heads, head_dim]")
+        _require(value.dim() == 3 and value.shape == key.shape, "value: the key's shape")
+        q, k = qk_norm_rope(query, key, positions, inv_freq, interleaved=interleaved, rope_scale=rope_scale,
+                            q_weight=q_weight, k_weight=k_weight, eps=eps, stream=stream)
+        with _launching(q.device, stream):
+            value = value.half().contiguous()
+            self.k_codec.encode_slots(k, k_packed, k_norms, slot_mapping)
+            self.v_codec.encode_slots(value, v_packed, v_norms, slot_mapping)
+        return attend_window_paged(q, self.k_codec, self.v_codec, k_packed, k_norms, v_packed, v_norms, block_tables,
+                                   context_lens, window=window, sinks=sinks, q_offsets=q_offsets, max_q=max_q,
+                                   stream=stream)
+
 
 def attend_decode_paged(q, k_codec: TurboQuant, v_codec: TurboQuant, k_cache, k_norms, v_cache, v_norms,
                         block_tables, context_lens, out=None, workspace=None, stream=None):
@@ -351,3 +418,352 @@ def attend_decode_paged(q, k_codec: TurboQuant, v_codec: TurboQuant, k_cache, k_
     tq_attend_decode_paged(k_codec.ctx, v_codec.ctx, q, B, hq, hkv, k_cache, k_norms, v_cache, v_norms, num_blocks,
                            block_tables, max_blocks, context_lens, out, workspace, workspace.numel(), stream)
     return out
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """(inv_freq [rot_dim / 2] float64 on `device`, rope_scale) for
+    `qk_norm_rope`: f_i = base^(-2 i / rot_dim), stretched by `factor` for
+    contexts beyond the `original_len` positions of training.
+
+    scaling: None; "linear" (every frequency divided by factor); "ntk" (the
+    base grows so that the lowest frequency is divided by factor and the
+    highest kept); "yarn" (frequencies of more than beta_fast turns within
+    original_len kept, of fewer than beta_slow divided by factor, a ramp
+    between, and rope_scale 1 + 0.1 ln(factor)).
+    """
+    import math
+
+    import torch
+
+    _require(rot_dim >= 2 and rot_dim % 2 == 0, "rot_dim: even, at least 2")
+    _require(scaling in (None, "linear", "ntk", "yarn"), "scaling: None, 'linear', 'ntk' or 'yarn'")
+    _require(factor >= 1.0 and base > 1.0 and original_len > 0, "factor >= 1, base > 1, original_len > 0")
+    _require(scaling != "ntk" or rot_dim > 2, "ntk: rot_dim of at least 4")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    if scaling == "ntk":
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = float(base) ** (-2 * i / rot_dim)
+    scale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        _require(beta_fast > beta_slow > 0, "beta_fast > beta_slow > 0")
+        turns = original_len * f / (2 * math.pi)
+        # the ramp runs over the index i, between those at which a frequency turns beta_fast and beta_slow times
+        at = [rot_dim * math.log(original_len / (b * 2 * math.pi)) / (2 * math.log(base)) for b in (beta_fast, beta_slow)]
+        lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot_dim // 2 - 1)
+        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        f = f * (1 - ramp) + f / factor * ramp
+        scale = 0.1 * math.log(factor) + 1.0
+    return f.to(device), scale
+
+
+def _head_rows(t, name):
+    """Checks of a [T, H, d] view whose rows are dense and 16-byte aligned."""
+    s0, s1, s2 = t.stride()
+    _require(s2 == 1 and s0 % 8 == 0 and s1 % 8 == 0 and t.data_ptr() % 16 == 0,
+             f"{name}: dense rows, 16-byte aligned, strides multiples of 8 elements")
+    return s0, s1
+
+
+def qk_norm_rope(q, k, positions, inv_freq=None, *, interleaved: bool = False, rope_scale: float = 1.0,
+                 q_weight=None, k_weight=None, eps: float = 1e-6, out=None, stream=None):
+    """Norm of every query and key head and rotation by position.
+
+    q [T, Hq, d], k [T, Hkv, d] fp16 or bf16 (views of one projection's output
+    are fine: rows dense, strides multiples of 8); positions [T] int32;
+    inv_freq [rot / 2] float64 (`rope_frequencies`), None for no rotation;
+    interleaved pairs (2i, 2i + 1) or half layout (i, i + rot / 2); weights [d]
+    in q's dtype or float32, None for no norm of that tensor. Returns (q, k)
+    fp16 [T, H, d]: keys as `encode_slots` takes them, queries as the attention
+    calls do. `out` = (q_out, k_out), which may be q and k where they are
+    contiguous fp16.
+    """
+    import torch
+
+    half = torch.float16
+    _require(isinstance(q, torch.Tensor) and isinstance(k, torch.Tensor) and q.dim() == 3 and k.dim() == 3,
+             "q: [T, Hq, d]; k: [T, Hkv, d]")
+    T, hq, d = q.shape
+    hkv = k.shape[1]
+    _require(k.shape[0] == T and k.shape[2] == d, "q: [T, Hq, d]; k: [T, Hkv, d] with the same T and d")
+    _require(d in (64, 128, 256), f"head_dim: 64, 128 or 256, got {d}")
+    _require(hq > 0 and hkv > 0, "q, k: at least one head")
+    _require(q.dtype in (half, torch.bfloat16) and k.dtype == q.dtype,
+             f"q, k: both float16 or both bfloat16, got {q.dtype} and {k.dtype}")
+    qs, ks = _head_rows(q, "q"), _head_rows(k, "k")
+    _check(positions, "positions", torch.int32, numel=T)
+    rot = 0
+    named = [("q", q), ("k", k), ("positions", positions)]
+    if inv_freq is not None:
+        _check(inv_freq, "inv_freq", torch.float64)
+        rot = 2 * inv_freq.numel()
+        _require(rot <= d, f"inv_freq: at most {d // 2} frequencies, got {rot // 2}")
+        named.append(("inv_freq", inv_freq))
+    w_type = None
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _check(w, name, (q.dtype, torch.float32), numel=d)
+            _require(w.data_ptr() % 16 == 0, f"{name}: 16-byte aligned")
+            _require(w_type in (None, w.dtype), "q_weight, k_weight: the same dtype")
+            w_type = w.dtype
+            named.append((name, w))
+    _require(eps >= 0.0, "eps: >= 0")
+    if out is not None:
+        _check(out[0], "out q", half, shape=(T, hq, d))
+        _check(out[1], "out k", half, shape=(T, hkv, d))
+        named += [("out q", out[0]), ("out k", out[1])]
+    dev = _one_device(named)
+    with _launching(dev, stream):
+        qo, ko = out if out is not None else (torch.empty(T, hq, d, dtype=half, device=dev),
+                                              torch.empty(T, hkv, d, dtype=half, device=dev))
+        tq_qk_norm_rope(q, k, TQ_F16 if q.dtype == half else TQ_BF16, T, hq, hkv, d, qs[0], qs[1], ks[0], ks[1],
+                        positions, inv_freq, rot, interleaved, rope_scale, q_weight, k_weight,
+                        w_type == torch.float32, eps, qo, ko)
+    return qo, ko
+
+
+def _window_args(q, k_codec, v_codec, q_offsets, max_q, n_seq, hkv, window, sinks, out, workspace):
+    import torch
+
+    T, hq, d = q.shape
+    _check(q, "q", torch.float16, shape=(T, hq, k_codec.head_dim))
+    _require(k_codec.head_dim == v_codec.head_dim, "k_codec, v_codec: the same head_dim")
+    _require(hkv > 0 and hq > 0 and hq % hkv == 0, f"q: a multiple of {hkv} heads, got {hq}")
+    _require(window is None or int(window) >= 1, "window: None or at least 1")
+    _require(int(sinks) >= 0, "sinks: at least 0")
+    named = [("q", q)]
+    if q_offsets is None:
+        _require(T == n_seq and max_q in (None, 1), "q: one token per sequence where q_offsets is None")
+        max_q = 1
+    else:
+        _check(q_offsets, "q_offsets", torch.int32, numel=n_seq + 1)
+        _require(max_q is not None and int(max_q) >= 1, "max_q: the largest number of tokens of a sequence")
+        named.append(("q_offsets", q_offsets))
+    if out is not None:
+        _check(out, "out", torch.float16, shape=(T, hq, d))
+        named.append(("out", out))
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8)
+        named.append(("workspace", workspace))
+    return T, hq, d, int(max_q), 0 if window is None else int(window), int(sinks), named
+
+
+def attend_window(q, k_codec: TurboQuant, v_codec: TurboQuant, k_packed, k_norms, v_packed, v_norms, context_lens,
+                  window=None, sinks: int = 0, q_offsets=None, max_q=None, out=None, workspace=None, stream=None):
+    """Causal attention of one or more query tokens per sequence over packed
+    caches, within the last `window` positions (None: all) and the first
+    `sinks`.
+
+    q [T, Hq, d] fp16; caches [B, S, Hkv, P] uint8 and norms [B, S, Hkv] f32 as
+    `attend_decode`; context_lens [B] int32, the query tokens included (their
+    keys and values are in the cache); q_offsets [B + 1] int32: sequence b's
+    tokens are q[q_offsets[b]:q_offsets[b + 1]], at most max_q of them (None:
+    one token per sequence). Returns o [T, Hq, d] fp16 (rows of tokens in no
+    sequence are not written).
+    """
+    import torch
+
+    _require(q.dim() == 3 and k_packed.dim() == 4, "q: [T, Hq, d]; k_packed: [B, S, Hkv, Pk]")
+    B, s_max, hkv = k_packed.shape[0], k_packed.shape[1], k_packed.shape[2]
+    T, hq, d, max_q, window, sinks, named = _window_args(q, k_codec, v_codec, q_offsets, max_q, B, hkv, window, sinks,
+                                                         out, workspace)
+    _check(k_packed, "k_packed", torch.uint8, shape=(B, s_max, hkv, k_codec.packed_bytes))
+    _check(v_packed, "v_packed", torch.uint8, shape=(B, s_max, hkv, v_codec.packed_bytes))
+    _check(k_norms, "k_norms", torch.float32, shape=(B, s_max, hkv))
+    _check(v_norms, "v_norms", torch.float32, shape=(B, s_max, hkv))
+    _check(context_lens, "context_lens", torch.int32, numel=B)
+    dev = _one_device(named + [("k_packed", k_packed), ("v_packed", v_packed), ("k_norms", k_norms),
+                               ("v_norms", v_norms), ("context_lens", context_lens)])
+    need = tq_attend_window_workspace_bytes(T, B, max_q, hq, hkv, d, s_max, window, sinks)
+    with _launching(dev, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        tq_attend_window(k_codec.ctx, v_codec.ctx, q, T, B, q_offsets, max_q, hq, hkv, k_packed, k_norms, v_packed,
+                         v_norms, s_max, context_lens, window, sinks, out, workspace,
+                         0 if workspace is None else workspace.numel())
+    return out
+
+
+def attend_window_paged(q, k_codec: TurboQuant, v_codec: TurboQuant, k_cache, k_norms, v_cache, v_norms,
+                        block_tables, context_lens, window=None, sinks: int = 0, q_offsets=None, max_q=None,
+                        out=None, workspace=None, stream=None):
+    """`attend_window` over paged caches: pools [num_blocks, 16, Hkv, P] and
+    block_tables [B, max_blocks] int32 as `attend_decode_paged`. Table entries
+    of pages that no query sees are not read, so they may be negative
+    (`pages_trim`)."""
+    import torch
+
+    _require(q.dim() == 3 and k_cache.dim() == 4 and block_tables.dim() == 2,
+             "q: [T, Hq, d]; k_cache: [num_blocks, 16, Hkv, Pk]; block_tables: [B, max_blocks]")
+    num_blocks, blk, hkv = k_cache.shape[0], k_cache.shape[1], k_cache.shape[2]
+    _require(blk == TQ_PAGE_BLOCK, f"cache blocks must hold {TQ_PAGE_BLOCK} positions")
+    B, max_blocks = block_tables.shape
+    T, hq, d, max_q, window, sinks, named = _window_args(q, k_codec, v_codec, q_offsets, max_q, B, hkv, window, sinks,
+                                                         out, workspace)
+    _check(k_cache, "k_cache", torch.uint8, shape=(num_blocks, blk, hkv, k_codec.packed_bytes))
+    _check(v_cache, "v_cache", torch.uint8, shape=(num_blocks, blk, hkv, v_codec.packed_bytes))
+    _check(k_norms, "k_norms", torch.float32, shape=(num_blocks, blk, hkv))
+    _check(v_norms, "v_norms", torch.float32, shape=(num_blocks, blk, hkv))
+    _check(block_tables, "block_tables", torch.int32)
+    _check(context_lens, "context_lens", torch.int32, numel=B)
+    dev = _one_device(named + [("k_cache", k_cache), ("v_cache", v_cache), ("k_norms", k_norms),
+                               ("v_norms", v_norms), ("block_tables", block_tables), ("context_lens", context_lens)])
+    need = tq_attend_window_workspace_bytes(T, B, max_q, hq, hkv, d, max_blocks * TQ_PAGE_BLOCK, window, sinks)
+    with _launching(dev, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        tq_attend_window_paged(k_codec.ctx, v_codec.ctx, q, T, B, q_offsets, max_q, hq, hkv, k_cache, k_norms,
+                               v_cache, v_norms, num_blocks, block_tables, max_blocks, context_lens, window, sinks,
+                               out, workspace, 0 if workspace is None else workspace.numel())
+    return out
+
+
+def _page_state(block_tables, context_lens, refs, num_blocks):
+    """Checks of the tables of a paged cache; (rows, max_blocks)."""
+    import torch
+
+    _check(block_tables, "block_tables", torch.int32)
+    _require(block_tables.dim() == 2 and block_tables.shape[0] > 0 and block_tables.shape[1] > 0,
+             "block_tables: [rows, max_blocks]")
+    if context_lens is not None:
+        _check(context_lens, "context_lens", torch.int32, numel=block_tables.shape[0])
+    _check(refs, "refs", torch.int32)
+    _require(refs.dim() == 1 and refs.numel() > 0 and num_blocks in (None, refs.numel()),
+             f"refs: one count per page ({num_blocks}), got {tuple(refs.shape)}")
+    return block_tables.shape[0], block_tables.shape[1]
+
+
+def pages_trim(block_tables, context_lens, refs, window=None, sinks: int = 0, release=None, out=None, stream=None):
+    """Give pages back: all pages of rows with release[row] true (their length
+    becomes 0), and of the others those that no query of `attend_window_paged`
+    with this window and sinks sees any more (window None: none of them).
+
+    block_tables [rows, max_blocks], context_lens [rows], refs [num_blocks]
+    int32; release [rows] bool or uint8, or None. Returns new (block_tables,
+    context_lens, refs), written to `out` where given (its tensors may be the
+    inputs themselves).
+    """
+    import torch
+
+    rows, max_blocks = _page_state(block_tables, context_lens, refs, None)
+    _require(window is None or int(window) >= 0, "window: None or at least 0")
+    _require(int(sinks) >= 0, "sinks: at least 0")
+    named = [("block_tables", block_tables), ("context_lens", context_lens), ("refs", refs)]
+    if release is not None:
+        _check(release, "release", (torch.bool, torch.uint8), numel=rows)
+        named.append(("release", release))
+    if out is not None:
+        _page_state(*out, refs.numel())
+        _require(out[0].shape == block_tables.shape, "out: tables of the same shape")
+        named += [("out", t) for t in out]
+    dev = _one_device(named)
+    with _launching(dev, stream):
+        t, n, r = out if out is not None else (torch.empty_like(block_tables), torch.empty_like(context_lens),
+                                               torch.empty_like(refs))
+        tq_pages_trim(block_tables, t, context_lens, n, refs, r, rows, max_blocks, refs.numel(),
+                      -1 if window is None else int(window), int(sinks), release)
+    return t, n, r
+
+
+class TQPagePools:
+    """The pools of a paged cache that share one page numbering: codes and
+    norms, keys and values, of every layer. `tensors`: contiguous CUDA tensors
+    [num_blocks, ...] on one device, each page a multiple of 16 bytes (views of
+    stacked layers are fine). Holds references to them."""
+
+    def __init__(self, tensors):
+        import torch
+
+        tensors = list(tensors)
+        _require(0 < len(tensors) <= TQ_MAX_PAGE_POOLS, f"pools: 1 to {TQ_MAX_PAGE_POOLS} tensors, got {len(tensors)}")
+        for i, t in enumerate(tensors):
+            _require(isinstance(t, torch.Tensor) and t.dim() >= 1 and t.numel() > 0, f"pool {i}: a tensor with pages")
+            _require(t.is_contiguous(), f"pool {i}: contiguous")
+            _require(t.shape[0] == tensors[0].shape[0], f"pool {i}: {tensors[0].shape[0]} pages, got {t.shape[0]}")
+            _require(t.data_ptr() % 16 == 0, f"pool {i}: 16-byte aligned")
+            size = t.numel() // t.shape[0] * t.element_size()
+            _require(size % 16 == 0, f"pool {i}: pages of a multiple of 16 bytes, got {size}")
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors)
+        _require(all(a[1] <= b[0] for a, b in zip(spans, spans[1:])), "pools: tensors that do not overlap")
+        self.device = _one_device([(f"pool {i}", t) for i, t in enumerate(tensors)])
+        self.tensors = tensors
+        self.num_blocks = tensors[0].shape[0]
+        self._array = (PagePool * len(tensors))()
+        for i, t in enumerate(tensors):
+            self._array[i].base = t.data_ptr()
+            self._array[i].block_bytes = t.numel() // t.shape[0] * t.element_size()
+
+    def _on_mine(self, named):
+        dev = _one_device(named)
+        _require(dev == self.device, f"tensors on {self.device} like the pools, got {dev}")
+        return dev
+
+    def fork(self, block_tables, context_lens, refs, parents, children, out=None, workspace=None, stream=None):
+        """Make row children[i] a copy of row parents[i]: the parent's full
+        pages are shared, a partly filled last page is copied to the lowest
+        free page. parents, children [n] int32; other tensors as `pages_trim`.
+        A child's former pages are not given back (`pages_trim` first). Returns
+        (block_tables, context_lens, refs)."""
+        import torch
+
+        rows, max_blocks = _page_state(block_tables, context_lens, refs, self.num_blocks)
+        n = parents.numel()
+        _check(parents, "parents", torch.int32)
+        _check(children, "children", torch.int32, numel=n)
+        _require(n <= rows <= TQ_MAX_PAGE_ROWS, f"at most {rows} forks of at most {TQ_MAX_PAGE_ROWS} rows")
+        named = [("block_tables", block_tables), ("context_lens", context_lens), ("refs", refs),
+                 ("parents", parents), ("children", children)]
+        if out is not None:
+            _page_state(*out, self.num_blocks)
+            _require(out[0].shape == block_tables.shape, "out: tables of the same shape")
+            named += [("out", t) for t in out]
+        if workspace is not None:
+            _check(workspace, "workspace", torch.uint8)
+            named.append(("workspace", workspace))
+        dev = self._on_mine(named)
+        with _launching(dev, stream):
+            t, c, r = out if out is not None else (torch.empty_like(block_tables), torch.empty_like(context_lens),
+                                                   torch.empty_like(refs))
+            if workspace is None:
+                workspace = torch.empty(tq_pages_fork_workspace_bytes(n), dtype=torch.uint8, device=dev)
+            tq_pages_fork(self._array, len(self._array), self.num_blocks, block_tables, t, context_lens, c, refs, r,
+                          rows, max_blocks, parents, children, n, workspace, workspace.numel())
+        return t, c, r
+
+    def compact(self, block_tables, refs, out=None, workspace=None, stream=None):
+        """Move the used pages (refs > 0) to the front of the pools. Returns
+        (block_tables, refs, remap, used): the tables with the new page
+        numbers, the moved counts, the new number of every page (-1: free) and
+        the number of used pages [1] int32. `out` = (block_tables, refs, remap,
+        used); the first two may be the inputs themselves."""
+        import torch
+
+        rows, max_blocks = _page_state(block_tables, None, refs, self.num_blocks)
+        _require(rows <= TQ_MAX_PAGE_ROWS, f"block_tables: at most {TQ_MAX_PAGE_ROWS} rows")
+        named = [("block_tables", block_tables), ("refs", refs)]
+        if out is not None:
+            _page_state(out[0], None, out[1], self.num_blocks)
+            _require(out[0].shape == block_tables.shape, "out: tables of the same shape")
+            _check(out[2], "out remap", torch.int32, numel=self.num_blocks)
+            _check(out[3], "out used", torch.int32, numel=1)
+            named += [("out", t) for t in out]
+        if workspace is not None:
+            _check(workspace, "workspace", torch.uint8)
+            named.append(("workspace", workspace))
+        dev = self._on_mine(named)
+        with _launching(dev, stream):
+            t, r, m, u = out if out is not None else (torch.empty_like(block_tables), torch.empty_like(refs),
+                                                      torch.empty_like(refs),
+                                                      torch.empty(1, dtype=torch.int32, device=dev))
+            if workspace is None:
+                workspace = torch.empty(tq_pages_compact_workspace_bytes(self.num_blocks), dtype=torch.uint8,
+                                        device=dev)
+            tq_pages_compact(self._array, len(self._array), self.num_blocks, block_tables, t, refs, r, rows,
+                             max_blocks, m, u, workspace, workspace.numel())
+        return t, r, m, u

@@ -46,6 +46,22 @@ _PROTOS = {
                                          _vp, _vp, _vp]),
     "tq_attend_decode_paged": (_c_int, [_vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _c_i64, _vp,
                                         _c_int, _vp, _vp, _vp, _c_size, _vp]),
+    "tq_qk_norm_rope": (_c_int, [_vp, _vp, _c_int, _c_i64, _c_int, _c_int, _c_int, _c_i64, _c_i64, _c_i64, _c_i64,
+                                 _vp, _vp, _c_int, _c_int, ctypes.c_float, _vp, _vp, _c_int, ctypes.c_float, _vp, _vp,
+                                 _vp]),
+    "tq_attend_window_workspace_bytes": (_c_size, [_c_i64, _c_int, _c_int, _c_int, _c_int, _c_int, _c_i64, _c_i64,
+                                                   _c_i64]),
+    "tq_attend_window": (_c_int, [_vp, _vp, _vp, _c_i64, _c_int, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp,
+                                  _c_i64, _vp, _c_i64, _c_i64, _vp, _vp, _c_size, _vp]),
+    "tq_attend_window_paged": (_c_int, [_vp, _vp, _vp, _c_i64, _c_int, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp,
+                                        _vp, _c_i64, _vp, _c_int, _vp, _c_i64, _c_i64, _vp, _vp, _c_size, _vp]),
+    "tq_pages_fork_workspace_bytes": (_c_size, [_c_int]),
+    "tq_pages_fork": (_c_int, [_vp, _c_int, _c_i64, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _vp, _vp, _c_int,
+                               _vp, _c_size, _vp]),
+    "tq_pages_trim": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_i64, _c_i64, _c_i64, _vp, _vp]),
+    "tq_pages_compact_workspace_bytes": (_c_size, [_c_i64]),
+    "tq_pages_compact": (_c_int, [_vp, _c_int, _c_i64, _vp, _vp, _vp, _vp, _c_int, _c_int, _vp, _vp, _vp, _c_size,
+                                  _vp]),
     "tq_device_error": (_c_int, [_vp, ctypes.POINTER(ctypes.c_uint32)]),
     "tq_check_device_error": (_c_int, [_vp]),
     "tq_tensor_core_check": (_c_int, [ctypes.POINTER(_c_int)]),
@@ -99,7 +115,13 @@ TQ_DEVERR_SLOT_RANGE = 0x2
 TQ_DEVERR_POS_RANGE = 0x4
 TQ_DEVERR_SMEM_LAYOUT = 0x8
 TQ_DEVERR_BLOCK_RANGE = 0x10
+TQ_DEVERR_ROW_RANGE = 0x20
+TQ_DEVERR_POOL_FULL = 0x40
 TQ_PAGE_BLOCK = 16
+TQ_MAX_PAGE_POOLS = 512
+TQ_MAX_PAGE_ROWS = 131072
+TQ_F16 = 0
+TQ_BF16 = 1
 
 LIB_PATH = _LIB_PATH
 
@@ -254,6 +276,77 @@ def tq_attend_decode_static(k: Ctx, v: Ctx, q, B: int, hq: int, hkv: int, k_pack
 
 
 TQ_ATTEND_STATIC_SCRATCH_BYTES = 8 << 20
+
+
+class PagePool(ctypes.Structure):
+    """tq_page_pool: base address and bytes of a page."""
+
+    _fields_ = [("base", _vp), ("block_bytes", _c_i64)]
+
+
+def tq_qk_norm_rope(q, k, dtype: int, n_tok: int, hq: int, hkv: int, head_dim: int, q_tok_stride: int,
+                    q_head_stride: int, k_tok_stride: int, k_head_stride: int, positions, inv_freq, rot_dim: int,
+                    interleaved: bool, rope_scale: float, q_weight, k_weight, weight_f32: bool, eps: float, q_out,
+                    k_out, stream=None) -> None:
+    _check(_lib.tq_qk_norm_rope(_ptr(q), _ptr(k), dtype, n_tok, hq, hkv, head_dim, q_tok_stride, q_head_stride,
+                                k_tok_stride, k_head_stride, _ptr(positions), _ptr(inv_freq), rot_dim,
+                                int(interleaved), rope_scale, _ptr(q_weight), _ptr(k_weight), int(weight_f32), eps,
+                                _ptr(q_out), _ptr(k_out), _stream(stream)), "tq_qk_norm_rope")
+
+
+def tq_attend_window_workspace_bytes(n_tok: int, B: int, max_q: int, hq: int, hkv: int, head_dim: int, s_max: int,
+                                     window: int, sinks: int) -> int:
+    return _lib.tq_attend_window_workspace_bytes(n_tok, B, max_q, hq, hkv, head_dim, s_max, window, sinks)
+
+
+def tq_attend_window(k: Ctx, v: Ctx, q, n_tok: int, B: int, q_offsets, max_q: int, hq: int, hkv: int, k_cache,
+                     k_norms, v_cache, v_norms, s_max: int, context_lens, window: int, sinks: int, out, workspace,
+                     ws_bytes: int, stream=None) -> None:
+    _check(_lib.tq_attend_window(k.handle, v.handle, _ptr(q), n_tok, B, _ptr(q_offsets), max_q, hq, hkv,
+                                 _ptr(k_cache), _ptr(k_norms), _ptr(v_cache), _ptr(v_norms), s_max,
+                                 _ptr(context_lens), window, sinks, _ptr(out), _ptr(workspace), ws_bytes,
+                                 _stream(stream)), "tq_attend_window")
+
+
+def tq_attend_window_paged(k: Ctx, v: Ctx, q, n_tok: int, B: int, q_offsets, max_q: int, hq: int, hkv: int, k_cache,
+                           k_norms, v_cache, v_norms, num_blocks: int, block_tables, max_blocks: int, context_lens,
+                           window: int, sinks: int, out, workspace, ws_bytes: int, stream=None) -> None:
+    _check(_lib.tq_attend_window_paged(k.handle, v.handle, _ptr(q), n_tok, B, _ptr(q_offsets), max_q, hq, hkv,
+                                       _ptr(k_cache), _ptr(k_norms), _ptr(v_cache), _ptr(v_norms), num_blocks,
+                                       _ptr(block_tables), max_blocks, _ptr(context_lens), window, sinks, _ptr(out),
+                                       _ptr(workspace), ws_bytes, _stream(stream)), "tq_attend_window_paged")
+
+
+def tq_pages_fork_workspace_bytes(n: int) -> int:
+    return _lib.tq_pages_fork_workspace_bytes(n)
+
+
+def tq_pages_fork(pools, n_pools: int, num_blocks: int, block_tables, tables_out, lens, lens_out, refs, refs_out,
+                  n_rows: int, max_blocks: int, parents, children, n: int, workspace, ws_bytes: int,
+                  stream=None) -> None:
+    """`pools`: a ctypes array of PagePool."""
+    _check(_lib.tq_pages_fork(pools, n_pools, num_blocks, _ptr(block_tables), _ptr(tables_out), _ptr(lens),
+                              _ptr(lens_out), _ptr(refs), _ptr(refs_out), n_rows, max_blocks, _ptr(parents),
+                              _ptr(children), n, _ptr(workspace), ws_bytes, _stream(stream)), "tq_pages_fork")
+
+
+def tq_pages_trim(block_tables, tables_out, lens, lens_out, refs, refs_out, n_rows: int, max_blocks: int,
+                  num_blocks: int, window: int, sinks: int, release, stream=None) -> None:
+    _check(_lib.tq_pages_trim(_ptr(block_tables), _ptr(tables_out), _ptr(lens), _ptr(lens_out), _ptr(refs),
+                              _ptr(refs_out), n_rows, max_blocks, num_blocks, window, sinks, _ptr(release),
+                              _stream(stream)), "tq_pages_trim")
+
+
+def tq_pages_compact_workspace_bytes(num_blocks: int) -> int:
+    return _lib.tq_pages_compact_workspace_bytes(num_blocks)
+
+
+def tq_pages_compact(pools, n_pools: int, num_blocks: int, block_tables, tables_out, refs, refs_out, n_rows: int,
+                     max_blocks: int, remap, used, workspace, ws_bytes: int, stream=None) -> None:
+    """`pools`: a ctypes array of PagePool."""
+    _check(_lib.tq_pages_compact(pools, n_pools, num_blocks, _ptr(block_tables), _ptr(tables_out), _ptr(refs),
+                                 _ptr(refs_out), n_rows, max_blocks, _ptr(remap), _ptr(used), _ptr(workspace),
+                                 ws_bytes, _stream(stream)), "tq_pages_compact")
 
 
 def tq_device_error(stream=None) -> tuple[int, int]:

@@ -1,0 +1,133 @@
+// Definitions shared by the kernels of windowed attention over packed caches
+// (tq_attend_window.cu: few query rows per kv head, on mma.sync;
+// tq_attend_window_tc.cu: many, on tcgen05) and their merge kernel: the launch
+// arguments, the rules for query rows and visible positions, and small helpers.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "tq_attend.cuh"
+
+namespace tq {
+
+struct AwArgs {
+  uint32_t k_sign_h2[TQ_MAX_D / 2];
+  uint32_t v_sign_h2[TQ_MAX_D / 2];
+  uint16_t k_lev[TQ_MAX_L];  // fp16 bits of lev_scale * level (tq_ctx::lev_f16)
+  uint16_t v_lev[TQ_MAX_L];
+  float q_scale;             // log2(e) / (d sqrt(d) K lev_scale)
+  float o_scale;             // 1 / (d V lev_scale)
+  const __half* q;           // [n_tok, hq, d]
+  __half* out;
+  const int32_t* q_offsets;  // [B + 1], or null: one token per sequence
+  const uint8_t* k_packed;
+  const float* k_norms;
+  const uint8_t* v_packed;
+  const float* v_norms;
+  const int32_t* block_tables;  // null: contiguous caches of s_max rows
+  const int32_t* ctx_lens;
+  int64_t s_max, num_blocks;
+  int64_t n_tok;
+  int max_blocks;
+  int B, max_q, hq, hkv, g;
+  int window, sinks;  // window: INT_MAX for none
+  int n_split;
+  float* ws_m;    // [n_tok * hq, n_split] running max (log2 domain)
+  float* ws_l;    // [n_tok * hq, n_split] sum of weights
+  float* ws_acc;  // [n_tok * hq, n_split, D] rotated accumulator
+  uint32_t* err;
+};
+
+// The sequence's first query token, its number of query tokens (0: nothing to
+// do) and its context length. Offsets that leave [0, n_tok], decrease or
+// exceed max_q are flagged and the sequence is left out.
+struct AwSeq {
+  int64_t q0;
+  int n, ctx;
+};
+TQ_DEV AwSeq aw_sequence(const AwArgs& a, int b, bool report) {
+  AwSeq s;
+  if (a.q_offsets) {
+    const int64_t lo = a.q_offsets[b], hi = a.q_offsets[b + 1];
+    s.q0 = lo;
+    s.n = (int)(hi - lo);
+    if (lo < 0 || hi < lo || hi > a.n_tok || hi - lo > a.max_q) {
+      if (report) record_error(a.err, TQ_DEVERR_ROW_RANGE);
+      s.n = 0;
+    }
+  } else {
+    s.q0 = b;
+    s.n = 1;
+  }
+  int64_t ctx = a.ctx_lens[b];
+  if (ctx > a.s_max) {
+    if (report) record_error(a.err, TQ_DEVERR_POS_RANGE);
+    ctx = a.s_max;
+  }
+  s.ctx = (int)(ctx < 0 ? 0 : ctx);
+  return s;
+}
+
+// Query token i of a sequence stands at position ctx - n + i (below 0: the row
+// sees nothing) and sees position t when t <= p and (t < sinks or
+// t > p - window).
+TQ_DEV int aw_position(const AwSeq& s, int i) { return max(s.ctx - s.n + i, -1); }
+TQ_DEV bool aw_visible(int t, int p, int window, int sinks) { return t <= p && (t < sinks || t > p - window); }
+
+// The 16-position blocks that queries at positions p_lo..p_hi see together:
+// the sinks' blocks [0, n_sink), then the window's from w0 on; n in all.
+struct AwBlocks {
+  int n_sink, w0, n;
+};
+TQ_DEV AwBlocks aw_blocks(int p_lo, int p_hi, int window, int sinks) {
+  AwBlocks r;
+  if (p_hi < 0) {
+    r.n_sink = r.w0 = r.n = 0;
+    return r;
+  }
+  const int lo = max(max(p_lo, 0) - window + 1, 0);  // first position of the window
+  const int last = p_hi / ATT_BLOCK;
+  r.w0 = lo / ATT_BLOCK;
+  r.n_sink = sinks > 0 ? min(min((sinks - 1) / ATT_BLOCK, last) + 1, r.w0) : 0;
+  r.n = r.n_sink + (last - r.w0 + 1);
+  return r;
+}
+TQ_DEV int aw_block(const AwBlocks& r, int m) { return m < r.n_sink ? m : r.w0 + (m - r.n_sink); }
+
+// Cache row (all kv heads) of the first position of block j of sequence b.
+TQ_DEV int64_t aw_block_row(const AwArgs& a, int b, int j) {
+  if (a.block_tables == nullptr) return (int64_t)b * a.s_max + (int64_t)j * ATT_BLOCK;
+  int64_t page = __ldg(a.block_tables + (int64_t)b * a.max_blocks + j);
+  if (page < 0 || page >= a.num_blocks) {
+    record_error(a.err, TQ_DEVERR_BLOCK_RANGE);
+    page = page < 0 ? 0 : a.num_blocks - 1;
+  }
+  return page * ATT_BLOCK;
+}
+
+TQ_DEV float aw_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Power of two that brings a positive magnitude into [2^10, 2^11) and its
+// inverse (1 for 0, infinities and NaN).
+TQ_DEV float aw_pow2_for(float mag, float& inv) {
+  const int e = (int)((__float_as_uint(mag) >> 23) & 255u);  // biased exponent
+  if (e == 0 || e == 255) {
+    inv = 1.f;
+    return 1.f;
+  }
+  const int up = min(max(10 - (e - 127), -126), 126);
+  inv = __uint_as_float((uint32_t)(127 - up) << 23);
+  return __uint_as_float((uint32_t)(127 + up) << 23);
+}
+
+}  // namespace tq
+
+// Merge of the splits (tq_attend_window.cu).
+cudaError_t tq_launch_window_combine(const tq::AwArgs& a, int d, cudaStream_t st);

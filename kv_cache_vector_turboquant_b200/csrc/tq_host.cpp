@@ -10,6 +10,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
 #include <new>
 
 #include "tq_internal.h"
@@ -86,6 +87,44 @@ bool choose_grid(const float* bounds, int nb, double* delta_out, double* frac_ou
   return false;
 }
 
+// The factor in [1, 2) that brings the codebook's levels nearest to fp16
+// values: the smallest largest relative error over 2^16 candidates, 1.7e-6 at
+// 2 bits, 1.5e-5 at 3 and 7.0e-5 at 4 (rounding them as they are: up to 2.4e-4).
+// A fixed function of the width: found once per width and process.
+double half_error(double x) {  // relative distance of x > 0 to the nearest 11-bit value
+  int e;
+  const double m = std::ldexp(std::frexp(x, &e), 11);
+  return std::fabs(std::nearbyint(m) - m) / m;
+}
+double level_scale(int bits, const float* levels) {
+  static std::once_flag once[TQ_MAX_BITS + 1];
+  static double found[TQ_MAX_BITS + 1];
+  std::call_once(once[bits], [&] {
+    const int L = 1 << bits;
+    double best = INFINITY;
+    for (int i = 0; i < 65536; ++i) {
+      const double f = 1.0 + i / 65536.0;
+      double worst = 0.0;
+      for (int k = L / 2; k < L && worst < best; ++k) worst = std::fmax(worst, half_error(f * levels[k]));
+      if (worst < best) {
+        best = worst;
+        found[bits] = f;
+      }
+    }
+  });
+  return found[bits];
+}
+// fp16 bits of x, 2^-14 <= |x| < 65504, rounded to nearest even.
+uint16_t half_bits(double x) {
+  int e;
+  double m = std::nearbyint(std::ldexp(std::frexp(std::fabs(x), &e), 11));  // in [1024, 2048]
+  if (m == 2048.0) {
+    m = 1024.0;
+    ++e;
+  }
+  return (uint16_t)((x < 0 ? 0x8000 : 0) | ((e + 14) << 10) | ((int)m - 1024));
+}
+
 bool valid_dims(int d, int bits) { return (d == 64 || d == 128 || d == 256) && bits >= 2 && bits <= 4; }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -132,6 +171,9 @@ tq_status tq_create(int head_dim, int bits, uint64_t seed, tq_ctx** out) {
   // levels on the 2^-14 grid (exact in f32), boundaries their midpoints (2^-15 grid)
   for (int k = 0; k < L; ++k) t.levels[k] = (float)(std::nearbyint(std::ldexp(c->lloyd_max[k], 14)) / 16384.0);
   for (int j = 0; j < L - 1; ++j) t.bounds[j] = 0.5f * (t.levels[j] + t.levels[j + 1]);
+  const double scale = level_scale(bits, t.levels);
+  c->lev_scale = (float)scale;  // a multiple of 2^-16: exact
+  for (int k = 0; k < L; ++k) c->lev_f16[k] = half_bits(scale * t.levels[k]);
 
   uint64_t state = seed;
   for (int i = 0; i < head_dim; i += 2) {
@@ -337,6 +379,151 @@ tq_status tq_attend_decode_paged(const tq_ctx* k, const tq_ctx* v, const void* q
   if (!aligned(workspace, 16)) return TQ_ERR_ALIGNMENT;
   return tq_launch_attend_paged(k, v, q_f16, B, hq, hkv, k_cache, k_norms, v_cache, v_norms, num_blocks,
                                 block_tables, max_blocks, context_lens, out_f16, workspace, ws_bytes, stream);
+}
+
+tq_status tq_qk_norm_rope(const void* q, const void* k, int dtype, int64_t n_tok, int hq, int hkv, int head_dim,
+                          int64_t q_tok_stride, int64_t q_head_stride, int64_t k_tok_stride, int64_t k_head_stride,
+                          const int32_t* positions, const double* inv_freq, int rot_dim, int interleaved,
+                          float rope_scale, const void* q_weight, const void* k_weight, int weight_f32, float eps,
+                          void* q_out, void* k_out, tq_stream stream) {
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return TQ_ERR_UNSUPPORTED;
+  if (dtype != TQ_F16 && dtype != TQ_BF16) return TQ_ERR_UNSUPPORTED;
+  if (n_tok < 0 || hq <= 0 || hkv <= 0 || rot_dim < 0 || rot_dim > head_dim || rot_dim % 2) return TQ_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || std::isinf(eps)) return TQ_ERR_INVALID_ARG;
+  if (n_tok == 0) return TQ_OK;
+  if (!q || !k || !q_out || !k_out || !positions || (rot_dim > 0 && !inv_freq)) return TQ_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(q_weight, 16) ||
+      !aligned(k_weight, 16) || !aligned(positions, 4) || !aligned(inv_freq, 8) ||
+      (q_tok_stride | q_head_stride | k_tok_stride | k_head_stride) % 8)
+    return TQ_ERR_ALIGNMENT;
+  if ((int64_t)hq + hkv > (1 << 20)) return TQ_ERR_UNSUPPORTED;
+  return tq_launch_norm_rope(q, k, dtype, n_tok, hq, hkv, head_dim, q_tok_stride, q_head_stride, k_tok_stride,
+                             k_head_stride, positions, inv_freq, rot_dim, interleaved, rope_scale, q_weight, k_weight,
+                             weight_f32, eps, q_out, k_out, stream);
+}
+
+size_t tq_attend_window_workspace_bytes(int64_t n_tok, int B, int max_q, int hq, int hkv, int head_dim, int64_t s_max,
+                                        int64_t window, int64_t sinks) {
+  if (n_tok <= 0 || B <= 0 || max_q <= 0 || hq <= 0 || hkv <= 0 || hq % hkv || s_max <= 0 || sinks < 0 ||
+      !(head_dim == 64 || head_dim == 128 || head_dim == 256))
+    return 0;
+  return tq_attend_window_workspace_impl(n_tok, B, max_q, hq, hkv, head_dim, s_max, window, sinks);
+}
+
+static tq_status attend_window(const tq_ctx* k, const tq_ctx* v, const void* q_f16, int64_t n_tok, int B,
+                               const int32_t* q_offsets, int max_q, int hq, int hkv, const void* k_cache,
+                               const float* k_norms, const void* v_cache, const float* v_norms, int64_t s_max,
+                               int64_t num_blocks, const int32_t* block_tables, int max_blocks,
+                               const int32_t* context_lens, int64_t window, int64_t sinks, void* out_f16,
+                               void* workspace, size_t ws_bytes, tq_stream stream) {
+  if (!k || !v) return TQ_ERR_INVALID_ARG;
+  if (k->d != v->d) return TQ_ERR_INVALID_ARG;
+  if (n_tok < 0 || B < 0 || max_q <= 0 || hq <= 0 || hkv <= 0 || hq % hkv != 0 || s_max <= 0 || sinks < 0)
+    return TQ_ERR_INVALID_ARG;
+  if (!q_offsets && (max_q != 1 || n_tok != B)) return TQ_ERR_INVALID_ARG;
+  if (B > 65535 || s_max >= ((int64_t)1 << 31) - 256) return TQ_ERR_UNSUPPORTED;
+  if (n_tok > 0x7fffffff || (int64_t)max_q * (hq / hkv) > 0x3fffffff) return TQ_ERR_UNSUPPORTED;
+  if (B == 0 || n_tok == 0) return TQ_OK;
+  if (!q_f16 || !k_cache || !k_norms || !v_cache || !v_norms || !context_lens || !out_f16) return TQ_ERR_INVALID_ARG;
+  if (!aligned(q_f16, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out_f16, 16) ||
+      !aligned(k_norms, 4) || !aligned(v_norms, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
+      !aligned(q_offsets, 4))
+    return TQ_ERR_ALIGNMENT;
+  const size_t need = tq_attend_window_workspace_bytes(n_tok, B, max_q, hq, hkv, k->d, s_max, window, sinks);
+  if (need > 0 && (!workspace || ws_bytes < need)) return TQ_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return TQ_ERR_ALIGNMENT;
+  return tq_launch_attend_window(k, v, q_f16, n_tok, B, q_offsets, max_q, hq, hkv, k_cache, k_norms, v_cache, v_norms,
+                                 s_max, num_blocks, block_tables, max_blocks, context_lens, window, sinks, out_f16,
+                                 workspace, stream);
+}
+
+tq_status tq_attend_window(const tq_ctx* k, const tq_ctx* v, const void* q_f16, int64_t n_tok, int B,
+                           const int32_t* q_offsets, int max_q, int hq, int hkv, const void* k_cache,
+                           const float* k_norms, const void* v_cache, const float* v_norms, int64_t s_max,
+                           const int32_t* context_lens, int64_t window, int64_t sinks, void* out_f16,
+                           void* workspace, size_t ws_bytes, tq_stream stream) {
+  return attend_window(k, v, q_f16, n_tok, B, q_offsets, max_q, hq, hkv, k_cache, k_norms, v_cache, v_norms, s_max, 0,
+                       nullptr, 0, context_lens, window, sinks, out_f16, workspace, ws_bytes, stream);
+}
+
+tq_status tq_attend_window_paged(const tq_ctx* k, const tq_ctx* v, const void* q_f16, int64_t n_tok, int B,
+                                 const int32_t* q_offsets, int max_q, int hq, int hkv, const void* k_cache,
+                                 const float* k_norms, const void* v_cache, const float* v_norms,
+                                 int64_t num_blocks, const int32_t* block_tables, int max_blocks,
+                                 const int32_t* context_lens, int64_t window, int64_t sinks, void* out_f16,
+                                 void* workspace, size_t ws_bytes, tq_stream stream) {
+  if (num_blocks <= 0 || max_blocks <= 0 || !block_tables) return TQ_ERR_INVALID_ARG;
+  if (num_blocks > ((int64_t)1 << 26)) return TQ_ERR_UNSUPPORTED;
+  return attend_window(k, v, q_f16, n_tok, B, q_offsets, max_q, hq, hkv, k_cache, k_norms, v_cache, v_norms,
+                       (int64_t)max_blocks * TQ_PAGE_BLOCK, num_blocks, block_tables, max_blocks, context_lens, window,
+                       sinks, out_f16, workspace, ws_bytes, stream);
+}
+
+// Checks shared by the page calls; TQ_OK when the arrays can be passed on.
+static tq_status check_pages(const tq_page_pool* pools, int n_pools, int64_t num_blocks, int n_rows, int max_blocks) {
+  if (n_pools < 0 || (n_pools > 0 && !pools) || num_blocks <= 0 || n_rows <= 0 || max_blocks <= 0)
+    return TQ_ERR_INVALID_ARG;
+  if (n_pools > TQ_MAX_PAGE_POOLS || num_blocks > ((int64_t)1 << 26) || n_rows > TQ_MAX_PAGE_ROWS ||
+      max_blocks > 0x7fffffff / TQ_PAGE_BLOCK)
+    return TQ_ERR_UNSUPPORTED;
+  for (int i = 0; i < n_pools; ++i) {
+    if (!pools[i].base || pools[i].block_bytes <= 0) return TQ_ERR_INVALID_ARG;
+    if (pools[i].block_bytes >= ((int64_t)1 << 31)) return TQ_ERR_UNSUPPORTED;
+    if (!aligned(pools[i].base, 16) || pools[i].block_bytes % 16) return TQ_ERR_ALIGNMENT;
+  }
+  return TQ_OK;
+}
+
+size_t tq_pages_fork_workspace_bytes(int n) { return n <= 0 ? 0 : tq_pages_fork_workspace_impl(n); }
+
+tq_status tq_pages_fork(const tq_page_pool* pools, int n_pools, int64_t num_blocks, const int32_t* block_tables,
+                        int32_t* tables_out, const int32_t* lens, int32_t* lens_out, const int32_t* refs,
+                        int32_t* refs_out, int n_rows, int max_blocks, const int32_t* parents,
+                        const int32_t* children, int n, void* workspace, size_t ws_bytes, tq_stream stream) {
+  const tq_status st = check_pages(pools, n_pools, num_blocks, n_rows, max_blocks);
+  if (st != TQ_OK) return st;
+  if (n < 0 || n > n_rows) return TQ_ERR_INVALID_ARG;
+  if (!block_tables || !tables_out || !lens || !lens_out || !refs || !refs_out || (n > 0 && (!parents || !children)))
+    return TQ_ERR_INVALID_ARG;
+  if (!aligned(block_tables, 4) || !aligned(tables_out, 4) || !aligned(lens, 4) || !aligned(lens_out, 4) ||
+      !aligned(refs, 4) || !aligned(refs_out, 4) || !aligned(parents, 4) || !aligned(children, 4) ||
+      !aligned(workspace, 16))
+    return TQ_ERR_ALIGNMENT;
+  if (n > 0 && (!workspace || ws_bytes < tq_pages_fork_workspace_bytes(n))) return TQ_ERR_WORKSPACE;
+  return tq_launch_pages_fork(pools, n_pools, num_blocks, block_tables, tables_out, lens, lens_out, refs, refs_out,
+                              n_rows, max_blocks, parents, children, n, workspace, stream);
+}
+
+tq_status tq_pages_trim(const int32_t* block_tables, int32_t* tables_out, const int32_t* lens, int32_t* lens_out,
+                        const int32_t* refs, int32_t* refs_out, int n_rows, int max_blocks, int64_t num_blocks,
+                        int64_t window, int64_t sinks, const uint8_t* release, tq_stream stream) {
+  const tq_status st = check_pages(nullptr, 0, num_blocks, n_rows, max_blocks);
+  if (st != TQ_OK) return st;
+  if (sinks < 0) return TQ_ERR_INVALID_ARG;
+  if (!block_tables || !tables_out || !lens || !lens_out || !refs || !refs_out) return TQ_ERR_INVALID_ARG;
+  if (!aligned(block_tables, 4) || !aligned(tables_out, 4) || !aligned(lens, 4) || !aligned(lens_out, 4) ||
+      !aligned(refs, 4) || !aligned(refs_out, 4))
+    return TQ_ERR_ALIGNMENT;
+  return tq_launch_pages_trim(block_tables, tables_out, lens, lens_out, refs, refs_out, n_rows, max_blocks,
+                              num_blocks, window, sinks, release, stream);
+}
+
+size_t tq_pages_compact_workspace_bytes(int64_t num_blocks) {
+  return num_blocks <= 0 ? 0 : tq_pages_compact_workspace_impl(num_blocks);
+}
+
+tq_status tq_pages_compact(const tq_page_pool* pools, int n_pools, int64_t num_blocks, const int32_t* block_tables,
+                           int32_t* tables_out, const int32_t* refs, int32_t* refs_out, int n_rows, int max_blocks,
+                           int32_t* remap, int32_t* used, void* workspace, size_t ws_bytes, tq_stream stream) {
+  const tq_status st = check_pages(pools, n_pools, num_blocks, n_rows, max_blocks);
+  if (st != TQ_OK) return st;
+  if (!block_tables || !tables_out || !refs || !refs_out || !remap || !used) return TQ_ERR_INVALID_ARG;
+  if (!aligned(block_tables, 4) || !aligned(tables_out, 4) || !aligned(refs, 4) || !aligned(refs_out, 4) ||
+      !aligned(remap, 4) || !aligned(used, 4) || !aligned(workspace, 16))
+    return TQ_ERR_ALIGNMENT;
+  if (!workspace || ws_bytes < tq_pages_compact_workspace_bytes(num_blocks)) return TQ_ERR_WORKSPACE;
+  return tq_launch_pages_compact(pools, n_pools, num_blocks, block_tables, tables_out, refs, refs_out, n_rows,
+                                 max_blocks, remap, used, workspace, stream);
 }
 
 tq_status tq_device_error(tq_stream stream, uint32_t* bits) { return tq_read_error_word(stream, bits); }

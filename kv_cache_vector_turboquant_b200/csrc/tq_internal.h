@@ -8,6 +8,7 @@
 #include "tq.h"
 
 #define TQ_MAX_D 256
+#define TQ_MAX_BITS 4
 #define TQ_MAX_L 16
 #define TQ_MAX_CELLS 272
 
@@ -50,6 +51,11 @@ struct tq_ctx {
   uint64_t seed;
   double lloyd_max[TQ_MAX_L];  // unrounded fp64 Lloyd-Max levels
   tq_codec_tables t;
+  // fp16 bits of lev_scale * levels[k], and that factor in [1, 2): the one at
+  // which the products lie nearest to fp16 values (windowed attention's
+  // matrix operands; the factor is divided out in f32)
+  uint16_t lev_f16[TQ_MAX_L];
+  float lev_scale;
 };
 
 // Guard band of the encode quantizer in z units (N(0,1) scale). The f32 path
@@ -103,6 +109,36 @@ tq_status tq_launch_attend_paged(const tq_ctx* k, const tq_ctx* v, const void* q
                                  const float* v_norms, int64_t num_blocks, const int32_t* block_tables,
                                  int max_blocks, const int32_t* context_lens, void* out, void* workspace,
                                  size_t ws_bytes, void* stream);
+// Norm and rotation of query and key heads (tq_norm_rope.cu).
+tq_status tq_launch_norm_rope(const void* q, const void* k, int dtype, int64_t n_tok, int hq, int hkv, int d,
+                              int64_t q_tok_stride, int64_t q_head_stride, int64_t k_tok_stride,
+                              int64_t k_head_stride, const int32_t* positions, const double* inv_freq, int rot_dim,
+                              int interleaved, float rope_scale, const void* q_weight, const void* k_weight,
+                              int weight_f32, float eps, void* q_out, void* k_out, void* stream);
+// Windowed attention (tq_attend_window.cu): block_tables null for contiguous
+// caches; q_offsets null for one query token per sequence.
+size_t tq_attend_window_workspace_impl(int64_t n_tok, int B, int max_q, int hq, int hkv, int head_dim, int64_t s_max,
+                                       int64_t window, int64_t sinks);
+tq_status tq_launch_attend_window(const tq_ctx* k, const tq_ctx* v, const void* q, int64_t n_tok, int B,
+                                  const int32_t* q_offsets, int max_q, int hq, int hkv, const void* k_cache,
+                                  const float* k_norms, const void* v_cache, const float* v_norms, int64_t s_max,
+                                  int64_t num_blocks, const int32_t* block_tables, int max_blocks,
+                                  const int32_t* ctx_lens, int64_t window, int64_t sinks, void* out, void* workspace,
+                                  void* stream);
+// Pages of a paged cache (tq_pages.cu).
+size_t tq_pages_fork_workspace_impl(int n);
+size_t tq_pages_compact_workspace_impl(int64_t num_blocks);
+tq_status tq_launch_pages_fork(const tq_page_pool* pools, int n_pools, int64_t num_blocks, const int32_t* tables,
+                               int32_t* tables_out, const int32_t* lens, int32_t* lens_out, const int32_t* refs,
+                               int32_t* refs_out, int n_rows, int max_blocks, const int32_t* parents,
+                               const int32_t* children, int n, void* workspace, void* stream);
+tq_status tq_launch_pages_trim(const int32_t* tables, int32_t* tables_out, const int32_t* lens, int32_t* lens_out,
+                               const int32_t* refs, int32_t* refs_out, int n_rows, int max_blocks,
+                               int64_t num_blocks, int64_t window, int64_t sinks, const uint8_t* release,
+                               void* stream);
+tq_status tq_launch_pages_compact(const tq_page_pool* pools, int n_pools, int64_t num_blocks, const int32_t* tables,
+                                  int32_t* tables_out, const int32_t* refs, int32_t* refs_out, int n_rows,
+                                  int max_blocks, int32_t* remap, int32_t* used, void* workspace, void* stream);
 size_t tq_attend_workspace_bytes_impl(int B, int hq, int head_dim, int64_t s_max);
 // The fast attention kernel's shared-memory plan for head_dim d, hw kv heads
 // and nt column tiles per CTA, a paged or contiguous cache, `reserved` bytes

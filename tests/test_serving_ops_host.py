@@ -1,0 +1,198 @@
+"""Refusals and host arithmetic of the operators around the packed cache,
+without a GPU: every refusal happens before a CUDA call."""
+
+import ctypes
+import math
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def K():
+    import kv_cache_vector_turboquant_b200 as K
+
+    return K
+
+
+def _raises(fn, text):
+    with pytest.raises(ValueError, match=text):
+        fn()
+
+
+def test_norm_rope_refusals(K):
+    q, k = torch.zeros(5, 4, 128, dtype=torch.float16), torch.zeros(5, 2, 128, dtype=torch.float16)
+    pos = torch.zeros(5, dtype=torch.int32)
+    f, _ = K.rope_frequencies(128, device="cpu")
+    w = torch.ones(128)
+    f_ = K.qk_norm_rope
+    _raises(lambda: f_(q, k, pos, f), "CUDA")
+    _raises(lambda: f_(q[0], k, pos, f), "Hq")
+    _raises(lambda: f_(q, k[:4], pos, f), "same T")
+    _raises(lambda: f_(q[..., :96], k[..., :96], pos), "head_dim")
+    _raises(lambda: f_(q.float(), k, pos, f), "float16")
+    _raises(lambda: f_(q, k.bfloat16(), pos, f), "float16")
+    _raises(lambda: f_(q, k, pos.long(), f), "positions: dtype")
+    _raises(lambda: f_(q, k, pos[:4], f), "positions: 5 elements")
+    _raises(lambda: f_(q, k, pos, f.float()), "inv_freq: dtype")
+    _raises(lambda: f_(q, k, pos, torch.zeros(65, dtype=torch.float64)), "at most 64")
+    _raises(lambda: f_(q, k, pos, f, q_weight=w[:64]), "q_weight: 128")
+    _raises(lambda: f_(q, k, pos, f, q_weight=w, k_weight=w.half()), "same dtype")
+    _raises(lambda: f_(q, k, pos, f, q_weight=w.bfloat16()), "q_weight: dtype")
+    _raises(lambda: f_(q, k, pos, f, eps=-1.0), "eps")
+    _raises(lambda: f_(q, k, pos, f, eps=float("nan")), "eps")
+    _raises(lambda: f_(q, k, pos, f, out=(q, k.float())), "out k: dtype")
+    _raises(lambda: f_(q, k, pos, f, out=(q[:4], k)), "out q: shape")
+    wide = torch.zeros(5, 4, 132, dtype=torch.float16)[..., :128]
+    _raises(lambda: f_(wide, k, pos, f), "strides")
+    off = torch.zeros(5 * 4 * 128 + 1, dtype=torch.float16)[1:].view(5, 4, 128)
+    _raises(lambda: f_(off, k, pos, f), "16-byte")
+    _raises(lambda: f_(q.transpose(1, 2).contiguous().transpose(1, 2), k, pos, f), "dense rows")
+
+
+def test_frequencies(K):
+    f, s = K.rope_frequencies(64, 10000.0, device="cpu")
+    assert f.dtype == torch.float64 and f.shape == (32,) and s == 1.0
+    assert f[0] == 1.0 and math.isclose(f[31].item(), 10000.0 ** (-62 / 64), rel_tol=1e-14)
+    lin, s = K.rope_frequencies(64, 10000.0, "linear", 4.0, device="cpu")
+    assert torch.allclose(lin * 4, f, rtol=1e-14, atol=0) and s == 1.0
+    ntk, _ = K.rope_frequencies(64, 10000.0, "ntk", 4.0, device="cpu")
+    assert ntk[0] == 1.0 and math.isclose(ntk[31].item() * 4, f[31].item(), rel_tol=1e-12)
+    yarn, s = K.rope_frequencies(64, 10000.0, "yarn", 4.0, original_len=4096, device="cpu")
+    assert math.isclose(s, 1 + 0.1 * math.log(4.0))
+    turns = 4096 * f / (2 * math.pi)
+    assert torch.equal(yarn[turns > 64], f[turns > 64])          # fast ones kept
+    assert torch.allclose(yarn[turns < 0.5] * 4, f[turns < 0.5])  # slow ones stretched
+    assert (yarn <= f).all() and (yarn * 4 >= f * (1 - 1e-12)).all()
+    for bad in (lambda: K.rope_frequencies(3), lambda: K.rope_frequencies(64, scaling="other"),
+                lambda: K.rope_frequencies(64, scaling="linear", factor=0.5),
+                lambda: K.rope_frequencies(2, scaling="ntk", factor=2.0)):
+        with pytest.raises(ValueError):
+            bad()
+
+
+def test_window_refusals(K):
+    kc, vc = K.TurboQuant(128, 4), K.TurboQuant(128, 2)
+    B, S, hkv, hq = 2, 32, 2, 8
+    q = torch.zeros(B, hq, 128, dtype=torch.float16)
+    kp, vp = torch.zeros(B, S, hkv, 64, dtype=torch.uint8), torch.zeros(B, S, hkv, 32, dtype=torch.uint8)
+    kn, vn = torch.zeros(B, S, hkv), torch.zeros(B, S, hkv)
+    ctx, off = torch.zeros(B, dtype=torch.int32), torch.zeros(B + 1, dtype=torch.int32)
+    f = K.attend_window
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx), "CUDA")
+    _raises(lambda: f(q.bfloat16(), kc, vc, kp, kn, vp, vn, ctx), "q: dtype")
+    _raises(lambda: f(q[:, :7].contiguous(), kc, vc, kp, kn, vp, vn, ctx), "multiple of 2")
+    _raises(lambda: f(q, kc, K.TurboQuant(64, 2), kp, kn, vp, vn, ctx), "same head_dim")
+    _raises(lambda: f(q, kc, vc, vp, kn, vp, vn, ctx), "k_packed: shape")
+    _raises(lambda: f(q, kc, vc, kp, kn[:1], vp, vn, ctx), "k_norms: shape")
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn.double(), ctx), "v_norms: dtype")
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx.long()), "context_lens: dtype")
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, window=0), "window")
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, sinks=-1), "sinks")
+    _raises(lambda: f(torch.cat([q, q]), kc, vc, kp, kn, vp, vn, ctx), "one token per sequence")
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, max_q=2), "one token per sequence")
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, q_offsets=off), "max_q")
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, q_offsets=off[:2], max_q=1), "q_offsets: 3")
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, out=q.float()), "out: dtype")
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, workspace=kn), "workspace: dtype")
+    pool = [t.reshape(B * S // 16, 16, *t.shape[2:]) for t in (kp, kn, vp, vn)]
+    bt = torch.zeros(B, S // 16, dtype=torch.int32)
+    p = K.attend_window_paged
+    _raises(lambda: p(q, kc, vc, *pool, bt, ctx), "CUDA")
+    _raises(lambda: p(q, kc, vc, *pool, bt.long(), ctx), "block_tables: dtype")
+    _raises(lambda: p(q, kc, vc, pool[0].reshape(2, 32, 2, 64), *pool[1:], bt, ctx), "16 positions")
+    _raises(lambda: p(q, kc, vc, *pool, bt, ctx[:1]), "context_lens")
+    layer = K.TQPagedAttention(kc, hq, v_tq=vc)
+    key = torch.zeros(B, hkv, 128, dtype=torch.float16)
+    _raises(lambda: layer.step(q[:, :4], key, key, ctx, ctx, *pool, bt, ctx), "num_query_heads")
+    _raises(lambda: layer.step(q, key, key[:1], ctx, ctx, *pool, bt, ctx), "value")
+    _raises(lambda: layer.step(q, key, key, ctx, ctx, *pool, bt, ctx), "CUDA")
+
+
+def test_page_refusals(K):
+    t, n, r = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), torch.zeros(9, dtype=torch.int32)
+    f = K.pages_trim
+    _raises(lambda: f(t, n, r, window=5), "CUDA")
+    _raises(lambda: f(t.long(), n, r), "block_tables: dtype")
+    _raises(lambda: f(t[0], n, r), r"\[rows, max_blocks\]")
+    _raises(lambda: f(t[:, :0], n, r), "max_blocks")
+    _raises(lambda: f(t, n[:2], r), "context_lens: 3")
+    _raises(lambda: f(t, n, r[:0]), "refs")
+    _raises(lambda: f(t, n, r, window=-1), "window")
+    _raises(lambda: f(t, n, r, sinks=-1), "sinks")
+    _raises(lambda: f(t, n, r, release=n), "release: dtype")
+    _raises(lambda: f(t, n, r, out=(t[:2], n[:2], r)), "same shape")
+    _raises(lambda: f(t, n, r, out=(t, n, r[:5])), "refs")
+    P = K.TQPagePools
+    pool = torch.zeros(9, 16, 2, 16, dtype=torch.uint8)
+    _raises(lambda: P([]), "pools")
+    _raises(lambda: P([pool]), "CUDA")
+    _raises(lambda: P([pool, pool[:8]]), "9 pages")
+    _raises(lambda: P([pool[:, :8]]), "contiguous")
+    _raises(lambda: P([torch.zeros(9, 24, dtype=torch.uint8)]), "multiple of 16")
+    _raises(lambda: P([torch.zeros(9 * 32 + 8, dtype=torch.uint8)[8:].view(9, 32)]), "aligned")
+    _raises(lambda: P([pool, pool[:]]), "overlap")
+    _raises(lambda: P([torch.zeros(9, 16, dtype=torch.uint8) for _ in range(513)]), "512")
+
+
+def test_abi_refusals(K):
+    """The C entry points with host pointers that are never followed."""
+    L = K._binding._lib
+    buf = ctypes.create_string_buffer(4096)
+    p = (ctypes.addressof(buf) + 63) & ~63
+    kc, vc, small = K.tq_create(128, 4), K.tq_create(128, 2), K.tq_create(64, 2)
+
+    def nr(dtype=0, n=4, hq=2, hkv=1, d=128, strides=(256, 128, 128, 128), rot=64, eps=1e-6, q=p, qo=p, freq=p):
+        return L.tq_qk_norm_rope(q, p, dtype, n, hq, hkv, d, *strides, p, freq, rot, 0, 1.0, None, None, 0, eps, qo, p, None)
+
+    assert nr(n=0, q=None) == K.TQ_OK
+    assert nr(d=96) == nr(dtype=2) == K.TQ_ERR_UNSUPPORTED
+    assert nr(n=-1) == nr(hq=0) == nr(hkv=0) == nr(rot=63) == nr(rot=130) == nr(eps=-1.0) == K.TQ_ERR_INVALID_ARG
+    assert nr(eps=float("nan")) == nr(eps=float("inf")) == nr(q=None) == nr(freq=None) == K.TQ_ERR_INVALID_ARG
+    assert nr(q=p + 8) == nr(qo=p + 2) == nr(strides=(256, 128, 132, 128)) == nr(freq=p + 4) == K.TQ_ERR_ALIGNMENT
+
+    def aw(k=kc, v=vc, q=p, T=2, B=2, off=None, mq=1, hq=4, hkv=2, S=64, win=0, sinks=0, ws=p, wsn=1 << 40, ctx=p):
+        return L.tq_attend_window(k.handle if k else None, v.handle, q, T, B, off, mq, hq, hkv, p, p, p, p, S, ctx, win,
+                                  sinks, p, ws, wsn, None)
+
+    assert aw(T=0, B=0, q=None) == K.TQ_OK and aw(T=0, off=p, q=None) == K.TQ_OK
+    assert aw(k=None) == aw(v=small) == aw(hq=3) == aw(hkv=0) == aw(S=0) == aw(sinks=-1) == K.TQ_ERR_INVALID_ARG
+    assert aw(T=3) == aw(mq=2) == aw(mq=0) == aw(q=None) == aw(ctx=None) == aw(T=-1) == K.TQ_ERR_INVALID_ARG
+    assert aw(S=1 << 31) == aw(T=65536, B=65536) == K.TQ_ERR_UNSUPPORTED
+    assert aw(q=p + 2) == aw(ctx=p + 2) == aw(off=p + 2, mq=2) == aw(ws=p + 4) == K.TQ_ERR_ALIGNMENT
+    assert aw(ws=None) == aw(wsn=16) == K.TQ_ERR_WORKSPACE
+    ws = K.tq_attend_window_workspace_bytes
+    assert ws(2, 2, 1, 4, 2, 128, 64, 0, 0) > 0 and ws(2, 2, 1, 4, 3, 128, 64, 0, 0) == ws(0, 2, 1, 4, 2, 128, 64, 0, 0) == 0
+    # the window bounds the splits, and so the workspace
+    assert ws(2, 2, 1, 4, 2, 128, 1 << 20, 100, 4) < ws(2, 2, 1, 4, 2, 128, 1 << 20, 0, 0)
+
+    def pg(nb=8, bt=p, mb=2, win=1, sinks=0):
+        return L.tq_pages_trim(bt, p, p, p, p, p, 3, mb, nb, win, sinks, None, None)
+
+    assert pg(nb=0) == pg(bt=None) == pg(mb=0) == pg(sinks=-1) == K.TQ_ERR_INVALID_ARG
+    assert pg(nb=1 << 27) == pg(mb=1 << 28) == K.TQ_ERR_UNSUPPORTED and pg(bt=p + 2) == K.TQ_ERR_ALIGNMENT
+
+    def fk(base=p, size=32, n=2, rows=3, ws=p, wsn=1 << 20, npool=1):
+        a = (K.PagePool * 1)()
+        a[0].base, a[0].block_bytes = base, size
+        return L.tq_pages_fork(a, npool, 8, p, p, p, p, p, p, rows, 2, p, p, n, ws, wsn, None)
+
+    assert fk(base=None) == fk(size=0) == fk(n=4) == fk(n=-1) == fk(rows=0) == K.TQ_ERR_INVALID_ARG
+    assert fk(rows=1 << 18) == fk(npool=513) == fk(size=1 << 31) == K.TQ_ERR_UNSUPPORTED
+    assert fk(base=p + 8) == fk(size=24) == K.TQ_ERR_ALIGNMENT
+    assert fk(ws=None) == fk(wsn=15) == K.TQ_ERR_WORKSPACE
+    assert K.tq_pages_fork_workspace_bytes(0) == K.tq_pages_compact_workspace_bytes(0) == 0
+
+
+def test_plain_page_operations_agree_with_a_walk(K):
+    """The list implementations that the GPU tests compare with, by hand."""
+    import serving_ref as R
+
+    t, n, r, moves, skipped, full = R.fork([[3, 1], [-1, -1], [-1, -1]], [20, 0, 0], [0, 1, 0, 1], [0, 0], [1, 2])
+    assert t == [[3, 1], [3, 0], [3, 2]] and n == [20, 20, 20] and r == [1, 1, 1, 3]
+    assert moves == [(1, 0), (1, 2)] and (skipped, full) == (0, 0)
+    t, n, r = R.trim([[0, 1, 2, 3]], [50], [1, 1, 1, 1], 17, 4, None)
+    assert t == [[0, -1, 2, 3]] and r == [1, 0, 1, 1]  # page 1 ends at 32 <= 50 - 17; page 2 at 48
+    t, n, r = R.trim([[0, 1, 2, 3]], [50], [1, 1, 1, 1], 2, 4, None)
+    assert t == [[0, -1, -1, 3]] and r == [1, 0, 0, 1]
+    assert R.compact([[4, 0, 2]], [0, 1, 0, 1, 2]) == ([[2, -1, -1]], [0 + 1, 1, 2, 0, 0], [-1, 1, -1, 0, 2], 3, [(3, 0), (4, 2)])
