@@ -76,6 +76,12 @@ def _require(cond: bool, msg: str) -> None:
 def _check(t, name: str, dtypes, shape=None, numel=None) -> None:
     """Type, dtype, layout and size of a tensor argument; the device is
     checked separately (_on_device), after every size check."""
+    try:  # the common case first: a call of a decode step makes a dozen of these
+        if (t.dtype is dtypes and t.is_contiguous() and (shape is None or t.shape == shape)
+                and (numel is None or t.numel() == numel)):
+            return
+    except AttributeError:
+        pass
     import torch
 
     _require(isinstance(t, torch.Tensor), f"{name}: a torch tensor")
@@ -112,14 +118,31 @@ def _launching(device, stream):
                 yield
 
 
-def _one_device(tensors) -> "torch.device":
-    """The CUDA device that holds all the (name, tensor) pairs."""
-    first = None
-    for name, t in tensors:
-        _require(t.is_cuda, f"{name}: a CUDA tensor")
-        first = t.device if first is None else first
-        _require(t.device == first, f"{name}: on {first} like the other tensors, got {t.device}")
-    return first
+def _one_device(names, tensors) -> int:
+    """Index of the CUDA device that holds all the tensors (Nones are left out)."""
+    dev = tensors[0].get_device()
+    if dev >= 0:
+        for t in tensors:
+            if t is not None and t.get_device() != dev:
+                break
+        else:
+            return dev
+    for name, t in zip(names, tensors):
+        if t is not None:
+            _require(t.is_cuda, f"{name}: a CUDA tensor")
+            _require(t.get_device() == dev, f"{name}: on {tensors[0].device} like the other tensors, got {t.device}")
+    return dev
+
+
+def _run(dev: int, stream, call, *args):
+    """call(raw stream, *args) with device `dev` current, on `stream` or that
+    device's current stream; what `call` allocates belongs to the stream."""
+    import torch
+
+    if stream is None and torch.cuda.current_device() == dev:
+        return call(torch._C._cuda_getCurrentRawStream(dev), *args)
+    with _launching(torch.device("cuda", dev), stream):
+        return call(torch.cuda.current_stream().cuda_stream, *args)
 
 
 class TurboQuant:
@@ -495,33 +518,35 @@ def qk_norm_rope(q, k, positions, inv_freq=None, *, interleaved: bool = False, r
     qs, ks = _head_rows(q, "q"), _head_rows(k, "k")
     _check(positions, "positions", torch.int32, numel=T)
     rot = 0
-    named = [("q", q), ("k", k), ("positions", positions)]
     if inv_freq is not None:
         _check(inv_freq, "inv_freq", torch.float64)
         rot = 2 * inv_freq.numel()
         _require(rot <= d, f"inv_freq: at most {d // 2} frequencies, got {rot // 2}")
-        named.append(("inv_freq", inv_freq))
     w_type = None
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
-            _check(w, name, (q.dtype, torch.float32), numel=d)
+            _check(w, name, torch.float32 if w.dtype is torch.float32 else (q.dtype, torch.float32), numel=d)
             _require(w.data_ptr() % 16 == 0, f"{name}: 16-byte aligned")
-            _require(w_type in (None, w.dtype), "q_weight, k_weight: the same dtype")
+            _require(w_type is None or w_type is w.dtype, "q_weight, k_weight: the same dtype")
             w_type = w.dtype
-            named.append((name, w))
     _require(eps >= 0.0, "eps: >= 0")
+    qo, ko = out if out is not None else (None, None)
     if out is not None:
-        _check(out[0], "out q", half, shape=(T, hq, d))
-        _check(out[1], "out k", half, shape=(T, hkv, d))
-        named += [("out q", out[0]), ("out k", out[1])]
-    dev = _one_device(named)
-    with _launching(dev, stream):
-        qo, ko = out if out is not None else (torch.empty(T, hq, d, dtype=half, device=dev),
-                                              torch.empty(T, hkv, d, dtype=half, device=dev))
-        tq_qk_norm_rope(q, k, TQ_F16 if q.dtype == half else TQ_BF16, T, hq, hkv, d, qs[0], qs[1], ks[0], ks[1],
+        _check(qo, "out q", half, shape=(T, hq, d))
+        _check(ko, "out k", half, shape=(T, hkv, d))
+    dev = _one_device(("q", "k", "positions", "inv_freq", "q_weight", "k_weight", "out q", "out k"),
+                      (q, k, positions, inv_freq, q_weight, k_weight, qo, ko))
+
+    def call(raw, qo, ko):
+        if qo is None:
+            qo = torch.empty((T, hq, d), dtype=half, device=q.device)
+            ko = torch.empty((T, hkv, d), dtype=half, device=q.device)
+        tq_qk_norm_rope(q, k, TQ_F16 if q.dtype is half else TQ_BF16, T, hq, hkv, d, qs[0], qs[1], ks[0], ks[1],
                         positions, inv_freq, rot, interleaved, rope_scale, q_weight, k_weight,
-                        w_type == torch.float32, eps, qo, ko)
-    return qo, ko
+                        w_type is torch.float32, eps, qo, ko, raw)
+        return qo, ko
+
+    return _run(dev, stream, call, qo, ko)
 
 
 def _window_args(q, k_codec, v_codec, q_offsets, max_q, n_seq, hkv, window, sinks, out, workspace):
@@ -533,21 +558,17 @@ def _window_args(q, k_codec, v_codec, q_offsets, max_q, n_seq, hkv, window, sink
     _require(hkv > 0 and hq > 0 and hq % hkv == 0, f"q: a multiple of {hkv} heads, got {hq}")
     _require(window is None or int(window) >= 1, "window: None or at least 1")
     _require(int(sinks) >= 0, "sinks: at least 0")
-    named = [("q", q)]
     if q_offsets is None:
         _require(T == n_seq and max_q in (None, 1), "q: one token per sequence where q_offsets is None")
         max_q = 1
     else:
         _check(q_offsets, "q_offsets", torch.int32, numel=n_seq + 1)
         _require(max_q is not None and int(max_q) >= 1, "max_q: the largest number of tokens of a sequence")
-        named.append(("q_offsets", q_offsets))
     if out is not None:
         _check(out, "out", torch.float16, shape=(T, hq, d))
-        named.append(("out", out))
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8)
-        named.append(("workspace", workspace))
-    return T, hq, d, int(max_q), 0 if window is None else int(window), int(sinks), named
+    return T, hq, d, int(max_q), 0 if window is None else int(window), int(sinks)
 
 
 def attend_window(q, k_codec: TurboQuant, v_codec: TurboQuant, k_packed, k_norms, v_packed, v_norms, context_lens,
@@ -567,25 +588,29 @@ def attend_window(q, k_codec: TurboQuant, v_codec: TurboQuant, k_packed, k_norms
 
     _require(q.dim() == 3 and k_packed.dim() == 4, "q: [T, Hq, d]; k_packed: [B, S, Hkv, Pk]")
     B, s_max, hkv = k_packed.shape[0], k_packed.shape[1], k_packed.shape[2]
-    T, hq, d, max_q, window, sinks, named = _window_args(q, k_codec, v_codec, q_offsets, max_q, B, hkv, window, sinks,
-                                                         out, workspace)
+    T, hq, d, max_q, window, sinks = _window_args(q, k_codec, v_codec, q_offsets, max_q, B, hkv, window, sinks, out,
+                                                  workspace)
     _check(k_packed, "k_packed", torch.uint8, shape=(B, s_max, hkv, k_codec.packed_bytes))
     _check(v_packed, "v_packed", torch.uint8, shape=(B, s_max, hkv, v_codec.packed_bytes))
     _check(k_norms, "k_norms", torch.float32, shape=(B, s_max, hkv))
     _check(v_norms, "v_norms", torch.float32, shape=(B, s_max, hkv))
     _check(context_lens, "context_lens", torch.int32, numel=B)
-    dev = _one_device(named + [("k_packed", k_packed), ("v_packed", v_packed), ("k_norms", k_norms),
-                               ("v_norms", v_norms), ("context_lens", context_lens)])
+    dev = _one_device(("q", "q_offsets", "out", "workspace", "k_packed", "v_packed", "k_norms", "v_norms",
+                       "context_lens"),
+                      (q, q_offsets, out, workspace, k_packed, v_packed, k_norms, v_norms, context_lens))
     need = tq_attend_window_workspace_bytes(T, B, max_q, hq, hkv, d, s_max, window, sinks)
-    with _launching(dev, stream):
+
+    def call(raw, out, workspace):
         if out is None:
             out = torch.empty_like(q)
         if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         tq_attend_window(k_codec.ctx, v_codec.ctx, q, T, B, q_offsets, max_q, hq, hkv, k_packed, k_norms, v_packed,
                          v_norms, s_max, context_lens, window, sinks, out, workspace,
-                         0 if workspace is None else workspace.numel())
-    return out
+                         0 if workspace is None else workspace.numel(), raw)
+        return out
+
+    return _run(dev, stream, call, out, workspace)
 
 
 def attend_window_paged(q, k_codec: TurboQuant, v_codec: TurboQuant, k_cache, k_norms, v_cache, v_norms,
@@ -602,26 +627,30 @@ def attend_window_paged(q, k_codec: TurboQuant, v_codec: TurboQuant, k_cache, k_
     num_blocks, blk, hkv = k_cache.shape[0], k_cache.shape[1], k_cache.shape[2]
     _require(blk == TQ_PAGE_BLOCK, f"cache blocks must hold {TQ_PAGE_BLOCK} positions")
     B, max_blocks = block_tables.shape
-    T, hq, d, max_q, window, sinks, named = _window_args(q, k_codec, v_codec, q_offsets, max_q, B, hkv, window, sinks,
-                                                         out, workspace)
+    T, hq, d, max_q, window, sinks = _window_args(q, k_codec, v_codec, q_offsets, max_q, B, hkv, window, sinks, out,
+                                                  workspace)
     _check(k_cache, "k_cache", torch.uint8, shape=(num_blocks, blk, hkv, k_codec.packed_bytes))
     _check(v_cache, "v_cache", torch.uint8, shape=(num_blocks, blk, hkv, v_codec.packed_bytes))
     _check(k_norms, "k_norms", torch.float32, shape=(num_blocks, blk, hkv))
     _check(v_norms, "v_norms", torch.float32, shape=(num_blocks, blk, hkv))
     _check(block_tables, "block_tables", torch.int32)
     _check(context_lens, "context_lens", torch.int32, numel=B)
-    dev = _one_device(named + [("k_cache", k_cache), ("v_cache", v_cache), ("k_norms", k_norms),
-                               ("v_norms", v_norms), ("block_tables", block_tables), ("context_lens", context_lens)])
+    dev = _one_device(("q", "q_offsets", "out", "workspace", "k_cache", "v_cache", "k_norms", "v_norms",
+                       "block_tables", "context_lens"),
+                      (q, q_offsets, out, workspace, k_cache, v_cache, k_norms, v_norms, block_tables, context_lens))
     need = tq_attend_window_workspace_bytes(T, B, max_q, hq, hkv, d, max_blocks * TQ_PAGE_BLOCK, window, sinks)
-    with _launching(dev, stream):
+
+    def call(raw, out, workspace):
         if out is None:
             out = torch.empty_like(q)
         if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         tq_attend_window_paged(k_codec.ctx, v_codec.ctx, q, T, B, q_offsets, max_q, hq, hkv, k_cache, k_norms,
                                v_cache, v_norms, num_blocks, block_tables, max_blocks, context_lens, window, sinks,
-                               out, workspace, 0 if workspace is None else workspace.numel())
-    return out
+                               out, workspace, 0 if workspace is None else workspace.numel(), raw)
+        return out
+
+    return _run(dev, stream, call, out, workspace)
 
 
 def _page_state(block_tables, context_lens, refs, num_blocks):
@@ -654,21 +683,22 @@ def pages_trim(block_tables, context_lens, refs, window=None, sinks: int = 0, re
     rows, max_blocks = _page_state(block_tables, context_lens, refs, None)
     _require(window is None or int(window) >= 0, "window: None or at least 0")
     _require(int(sinks) >= 0, "sinks: at least 0")
-    named = [("block_tables", block_tables), ("context_lens", context_lens), ("refs", refs)]
     if release is not None:
-        _check(release, "release", (torch.bool, torch.uint8), numel=rows)
-        named.append(("release", release))
+        _check(release, "release", torch.bool if release.dtype is torch.bool else (torch.bool, torch.uint8), numel=rows)
     if out is not None:
         _page_state(*out, refs.numel())
         _require(out[0].shape == block_tables.shape, "out: tables of the same shape")
-        named += [("out", t) for t in out]
-    dev = _one_device(named)
-    with _launching(dev, stream):
+    dev = _one_device(("block_tables", "context_lens", "refs", "release", "out", "out", "out"),
+                      (block_tables, context_lens, refs, release, *(out if out is not None else ())))
+
+    def call(raw, out):
         t, n, r = out if out is not None else (torch.empty_like(block_tables), torch.empty_like(context_lens),
                                                torch.empty_like(refs))
         tq_pages_trim(block_tables, t, context_lens, n, refs, r, rows, max_blocks, refs.numel(),
-                      -1 if window is None else int(window), int(sinks), release)
-    return t, n, r
+                      -1 if window is None else int(window), int(sinks), release, raw)
+        return t, n, r
+
+    return _run(dev, stream, call, out)
 
 
 class TQPagePools:
@@ -691,7 +721,7 @@ class TQPagePools:
             _require(size % 16 == 0, f"pool {i}: pages of a multiple of 16 bytes, got {size}")
         spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors)
         _require(all(a[1] <= b[0] for a, b in zip(spans, spans[1:])), "pools: tensors that do not overlap")
-        self.device = _one_device([(f"pool {i}", t) for i, t in enumerate(tensors)])
+        self._dev = _one_device([f"pool {i}" for i in range(len(tensors))], tensors)
         self.tensors = tensors
         self.num_blocks = tensors[0].shape[0]
         self._array = (PagePool * len(tensors))()
@@ -699,10 +729,9 @@ class TQPagePools:
             self._array[i].base = t.data_ptr()
             self._array[i].block_bytes = t.numel() // t.shape[0] * t.element_size()
 
-    def _on_mine(self, named):
-        dev = _one_device(named)
-        _require(dev == self.device, f"tensors on {self.device} like the pools, got {dev}")
-        return dev
+    def _on_mine(self, names, tensors):
+        dev = _one_device(names, tensors)
+        _require(dev == self._dev, f"tensors on cuda:{self._dev} like the pools, got cuda:{dev}")
 
     def fork(self, block_tables, context_lens, refs, parents, children, out=None, workspace=None, stream=None):
         """Make row children[i] a copy of row parents[i]: the parent's full
@@ -717,24 +746,25 @@ class TQPagePools:
         _check(parents, "parents", torch.int32)
         _check(children, "children", torch.int32, numel=n)
         _require(n <= rows <= TQ_MAX_PAGE_ROWS, f"at most {rows} forks of at most {TQ_MAX_PAGE_ROWS} rows")
-        named = [("block_tables", block_tables), ("context_lens", context_lens), ("refs", refs),
-                 ("parents", parents), ("children", children)]
         if out is not None:
             _page_state(*out, self.num_blocks)
             _require(out[0].shape == block_tables.shape, "out: tables of the same shape")
-            named += [("out", t) for t in out]
         if workspace is not None:
             _check(workspace, "workspace", torch.uint8)
-            named.append(("workspace", workspace))
-        dev = self._on_mine(named)
-        with _launching(dev, stream):
+        self._on_mine(("block_tables", "context_lens", "refs", "parents", "children", "workspace", "out", "out", "out"),
+                      (block_tables, context_lens, refs, parents, children, workspace,
+                       *(out if out is not None else ())))
+
+        def call(raw, out, workspace):
             t, c, r = out if out is not None else (torch.empty_like(block_tables), torch.empty_like(context_lens),
                                                    torch.empty_like(refs))
             if workspace is None:
-                workspace = torch.empty(tq_pages_fork_workspace_bytes(n), dtype=torch.uint8, device=dev)
+                workspace = torch.empty(tq_pages_fork_workspace_bytes(n), dtype=torch.uint8, device=refs.device)
             tq_pages_fork(self._array, len(self._array), self.num_blocks, block_tables, t, context_lens, c, refs, r,
-                          rows, max_blocks, parents, children, n, workspace, workspace.numel())
-        return t, c, r
+                          rows, max_blocks, parents, children, n, workspace, workspace.numel(), raw)
+            return t, c, r
+
+        return _run(self._dev, stream, call, out, workspace)
 
     def compact(self, block_tables, refs, out=None, workspace=None, stream=None):
         """Move the used pages (refs > 0) to the front of the pools. Returns
@@ -746,24 +776,25 @@ class TQPagePools:
 
         rows, max_blocks = _page_state(block_tables, None, refs, self.num_blocks)
         _require(rows <= TQ_MAX_PAGE_ROWS, f"block_tables: at most {TQ_MAX_PAGE_ROWS} rows")
-        named = [("block_tables", block_tables), ("refs", refs)]
         if out is not None:
             _page_state(out[0], None, out[1], self.num_blocks)
             _require(out[0].shape == block_tables.shape, "out: tables of the same shape")
             _check(out[2], "out remap", torch.int32, numel=self.num_blocks)
             _check(out[3], "out used", torch.int32, numel=1)
-            named += [("out", t) for t in out]
         if workspace is not None:
             _check(workspace, "workspace", torch.uint8)
-            named.append(("workspace", workspace))
-        dev = self._on_mine(named)
-        with _launching(dev, stream):
+        self._on_mine(("block_tables", "refs", "workspace", "out", "out", "out", "out"),
+                      (block_tables, refs, workspace, *(out if out is not None else ())))
+
+        def call(raw, out, workspace):
             t, r, m, u = out if out is not None else (torch.empty_like(block_tables), torch.empty_like(refs),
                                                       torch.empty_like(refs),
-                                                      torch.empty(1, dtype=torch.int32, device=dev))
+                                                      torch.empty(1, dtype=torch.int32, device=refs.device))
             if workspace is None:
                 workspace = torch.empty(tq_pages_compact_workspace_bytes(self.num_blocks), dtype=torch.uint8,
-                                        device=dev)
+                                        device=refs.device)
             tq_pages_compact(self._array, len(self._array), self.num_blocks, block_tables, t, refs, r, rows,
-                             max_blocks, m, u, workspace, workspace.numel())
-        return t, r, m, u
+                             max_blocks, m, u, workspace, workspace.numel(), raw)
+            return t, r, m, u
+
+        return _run(self._dev, stream, call, out, workspace)

@@ -170,7 +170,7 @@ class Ctx:
 
     def __del__(self):
         h = getattr(self, "_h", None)
-        if h is not None and h.value:
+        if h is not None and h.value and _lib is not None:  # (None: the interpreter is shutting down)
             _lib.tq_destroy(h)
             self._h = ctypes.c_void_p(0)
 

@@ -26,7 +26,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtq.so")
 TEST_LIB = os.path.join(PKG, "libtq_test.so")
 
-SOURCES = ["tq_host.cpp", "tq_device.cu", "tq_encode.cu", "tq_encode_tc.cu", "tq_decode.cu", "tq_decode_tc.cu", "tq_attend.cu", "tq_attend_fast.cu", "tq_attend_static.cu", "tq_mma_check.cu", "tq_norm_rope.cu", "tq_attend_window.cu", "tq_pages.cu"]
+SOURCES = ["tq_host.cpp", "tq_device.cu", "tq_encode.cu", "tq_encode_tc.cu", "tq_decode.cu", "tq_decode_tc.cu", "tq_attend.cu", "tq_attend_fast.cu", "tq_attend_static.cu", "tq_mma_check.cu", "tq_norm_rope.cu", "tq_attend_window.cu", "tq_attend_window_tc.cu", "tq_pages.cu"]
 # test hooks (include/tq_test.h): a separate library, linked against libtq.so,
 # that the product path never loads
 TEST_SOURCES = ["tq_test_hooks.cpp", "tq_test_umma.cu"]

@@ -80,46 +80,6 @@ TQ_DEV void aw_build_tables(uint8_t* smem, const AwArgs& a) {
   }
 }
 
-// NBYTES bytes from byte `off` of a cache row as a little-endian word stream;
-// reads stay inside the row (rows are 8-byte aligned multiples of 8 bytes).
-template <int NBYTES, int NW>
-TQ_DEV void aw_load(uint32_t (&w)[NW], const uint8_t* row, int off, int row_bytes) {
-  static_assert(NW == (NBYTES + 3) / 4, "words of the stream");
-  if constexpr (NBYTES % 16 == 0) {
-#pragma unroll
-    for (int i = 0; i < NBYTES / 16; ++i) {
-      const uint4 r = __ldg(reinterpret_cast<const uint4*>(row + off) + i);
-      w[4 * i] = r.x, w[4 * i + 1] = r.y, w[4 * i + 2] = r.z, w[4 * i + 3] = r.w;
-    }
-  } else if constexpr (NBYTES % 8 == 0) {
-#pragma unroll
-    for (int i = 0; i < NBYTES / 8; ++i) {
-      const uint2 r = __ldg(reinterpret_cast<const uint2*>(row + off) + i);
-      w[2 * i] = r.x, w[2 * i + 1] = r.y;
-    }
-  } else if constexpr (NBYTES % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < NBYTES / 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + off) + i);
-  } else if constexpr (NBYTES == 2) {
-    w[0] = __ldg(reinterpret_cast<const uint16_t*>(row + off));
-  } else {  // 3 or 6 bytes: two aligned words
-    const int base = off & ~3;
-    const uint32_t r0 = __ldg(reinterpret_cast<const uint32_t*>(row + base));
-    const uint32_t r1 = __ldg(reinterpret_cast<const uint32_t*>(row + min(base + 4, row_bytes - 4)));
-    const uint32_t sh = (uint32_t)(off & 3) * 8u;
-    w[0] = __funnelshift_r(r0, r1, sh);
-    if constexpr (NW > 1) w[1] = r1 >> sh;
-  }
-}
-
-// `NB` bits at bit `off` of a word stream (compile-time offsets).
-template <int NB, int N>
-TQ_DEV uint32_t aw_bits(const uint32_t (&w)[N], int off) {
-  uint32_t f = w[off >> 5] >> (off & 31);
-  if ((off & 31) + NB > 32 && (off >> 5) + 1 < N) f |= w[(off >> 5) + 1] << (32 - (off & 31));
-  return f & ((1u << NB) - 1u);
-}
-
 TQ_DEV uint32_t aw_transpose(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -200,7 +160,7 @@ __global__ void __launch_bounds__(AW_WARPS * 32, D == 256 || NT > 1 ? 1 : 2)
     mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
     mag = fmaxf(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
     float inv;
-    const float up = aw_pow2_for(mag, inv);
+    const float up = aw_pow2_for<10>(mag, inv);
     row_inv[j] = __shfl_sync(0xffffffffu, inv, 8 * tq);  // the lane whose column holds row tq
     const bool lo = gq & 1;
 #pragma unroll
@@ -329,7 +289,7 @@ __global__ void __launch_bounds__(AW_WARPS * 32, D == 256 || NT > 1 ? 1 : 2)
     if (nmax > v_most) {
       v_most = nmax;
       float inv;
-      const float up = aw_pow2_for(nmax, inv);
+      const float up = aw_pow2_for<10>(nmax, inv);
       v_fix = up * v_inv;  // <= 1 from the second time on
       v_up = up;
       v_inv = inv;
@@ -533,17 +493,25 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_consta
     dst[e / 2] = pack_half2(x[e] * inv, x[e + 1] * inv) ^ a.v_sign_h2[(lane * E + e) / 2];
 }
 
-// Splits of a call: enough warps to fill the SMs twice over, at least one step
-// of 32 positions each; from the sizes alone, so that the workspace is too.
+// Query rows per kv head from which the tensor-memory kernel takes a call.
+constexpr int64_t AW_TC_ROWS = 32;
+
+static bool window_tc(int hq, int hkv, int max_q) { return (int64_t)max_q * (hq / hkv) >= AW_TC_ROWS; }
+
+// Splits of a call, from the sizes alone, so that the workspace is too: this
+// kernel, enough warps to fill the SMs twice over, at least one step of 32
+// positions each; the tensor-memory kernel, one CTA per SM, at least four
+// tiles of 64 each.
 static int window_splits(int B, int hq, int hkv, int max_q, int d, int64_t s_max, int64_t window, int64_t sinks) {
-  const int rt = 4;
+  const bool tc = window_tc(hq, hkv, max_q);
+  const int64_t rt = tc ? tq_window_tc_rows(d) : 4;
   const int64_t tiles = ((int64_t)max_q * (hq / hkv) + rt - 1) / rt;
   const int64_t units = (int64_t)B * hkv * tiles;
   int64_t seen = s_max;
   if (window > 0) seen = std::min(seen, window + sinks + max_q + 2 * ATT_BLOCK);
-  const int64_t steps = (seen + AW_TILE - 1) / AW_TILE;
-  const int64_t want = std::max<int64_t>(1, (int64_t)(d == 256 ? 1 : 2) * 148 * AW_WARPS / units);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(want, steps));
+  const int64_t steps = tc ? (seen + 255) / 256 : (seen + AW_TILE - 1) / AW_TILE;
+  const int64_t slots = tc ? 148 : (d == 256 ? 1 : 2) * 148 * AW_WARPS;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(slots / units, steps));
 }
 
 template <int D, int KB, int VB, int NT>
@@ -646,7 +614,14 @@ tq_status tq_launch_attend_window(const tq_ctx* k, const tq_ctx* v, const void* 
   a.err = tq_error_word();
   if (!a.err) return TQ_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  a.wait_limit = TQ_WAIT_LIMIT_CYCLES;
   cudaError_t e = cudaErrorInvalidValue;
+  if (window_tc(hq, hkv, max_q)) {
+    e = tq_launch_window_tc(a, d, k->bits, v->bits, st);
+    if (e == cudaSuccess && a.n_split > 1) e = tq_launch_window_combine(a, d, st);
+    if (e == cudaErrorNotSupported) return TQ_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  }
   if (d == 64) e = launch_window_d<64>(a, k->bits, v->bits, st);
   if (d == 128) e = launch_window_d<128>(a, k->bits, v->bits, st);
   if (d == 256) e = launch_window_d<256>(a, k->bits, v->bits, st);

@@ -39,6 +39,7 @@ struct AwArgs {
   float* ws_l;    // [n_tok * hq, n_split] sum of weights
   float* ws_acc;  // [n_tok * hq, n_split, D] rotated accumulator
   uint32_t* err;
+  long long wait_limit;
 };
 
 // The sequence's first query token, its number of query tokens (0: nothing to
@@ -114,20 +115,66 @@ TQ_DEV float aw_exp2(float x) {
   return y;
 }
 
-// Power of two that brings a positive magnitude into [2^10, 2^11) and its
-// inverse (1 for 0, infinities and NaN).
+// Power of two that brings a positive magnitude into [2^TO, 2^(TO + 1)) and
+// its inverse (1 for 0, infinities and NaN).
+template <int TO>
 TQ_DEV float aw_pow2_for(float mag, float& inv) {
   const int e = (int)((__float_as_uint(mag) >> 23) & 255u);  // biased exponent
   if (e == 0 || e == 255) {
     inv = 1.f;
     return 1.f;
   }
-  const int up = min(max(10 - (e - 127), -126), 126);
+  const int up = min(max(TO - (e - 127), -126), 126);
   inv = __uint_as_float((uint32_t)(127 - up) << 23);
   return __uint_as_float((uint32_t)(127 + up) << 23);
 }
 
+// NBYTES bytes from byte `off` of a cache row as a little-endian word stream;
+// reads stay inside the row (rows are 8-byte aligned multiples of 8 bytes).
+template <int NBYTES, int NW>
+TQ_DEV void aw_load(uint32_t (&w)[NW], const uint8_t* row, int off, int row_bytes) {
+  static_assert(NW == (NBYTES + 3) / 4, "words of the stream");
+  if constexpr (NBYTES % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < NBYTES / 16; ++i) {
+      const uint4 r = __ldg(reinterpret_cast<const uint4*>(row + off) + i);
+      w[4 * i] = r.x, w[4 * i + 1] = r.y, w[4 * i + 2] = r.z, w[4 * i + 3] = r.w;
+    }
+  } else if constexpr (NBYTES % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < NBYTES / 8; ++i) {
+      const uint2 r = __ldg(reinterpret_cast<const uint2*>(row + off) + i);
+      w[2 * i] = r.x, w[2 * i + 1] = r.y;
+    }
+  } else if constexpr (NBYTES % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < NBYTES / 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + off) + i);
+  } else if constexpr (NBYTES == 2) {
+    w[0] = __ldg(reinterpret_cast<const uint16_t*>(row + off));
+  } else {  // 3 or 6 bytes: two aligned words
+    const int base = off & ~3;
+    const uint32_t r0 = __ldg(reinterpret_cast<const uint32_t*>(row + base));
+    const uint32_t r1 = __ldg(reinterpret_cast<const uint32_t*>(row + min(base + 4, row_bytes - 4)));
+    const uint32_t sh = (uint32_t)(off & 3) * 8u;
+    w[0] = __funnelshift_r(r0, r1, sh);
+    if constexpr (NW > 1) w[1] = r1 >> sh;
+  }
+}
+
+// `NB` bits at bit `off` of a word stream (compile-time offsets).
+template <int NB, int N>
+TQ_DEV uint32_t aw_bits(const uint32_t (&w)[N], int off) {
+  uint32_t f = w[off >> 5] >> (off & 31);
+  if ((off & 31) + NB > 32 && (off >> 5) + 1 < N) f |= w[(off >> 5) + 1] << (32 - (off & 31));
+  return f & ((1u << NB) - 1u);
+}
+
 }  // namespace tq
+
+// The kernel for many query rows per kv head (tq_attend_window_tc.cu): rows of
+// a CTA, and its launch.
+int tq_window_tc_rows(int d);
+cudaError_t tq_launch_window_tc(const tq::AwArgs& a, int d, int k_bits, int v_bits, cudaStream_t st);
 
 // Merge of the splits (tq_attend_window.cu).
 cudaError_t tq_launch_window_combine(const tq::AwArgs& a, int d, cudaStream_t st);

@@ -1,0 +1,647 @@
+// Windowed attention over packed caches for many query rows per kv head
+// (prompt chunks, drafted tokens of wide head groups) on the fifth-generation
+// tensor cores. The mathematics, the rotation of queries and output and the
+// precision are those of tq_attend_window.cu; here the codes become fp16
+// tiles in shared memory once and serve MT x 128 query rows.
+//
+// A CTA takes MT tiles of 128 query rows (row = token x query head of the
+// group) of one kv head and walks over the 64-position tiles that they see
+// (four 16-position blocks of the list sinks, window). Roles:
+//  * 4 warps turn key codes into level pairs (table lookups as in
+//    tq_attend_window.cu, 16 lane copies) and write them as a K-major,
+//    128-byte-swizzled operand [64 positions x d]; their first warp also puts
+//    the tile's norms and positions into a ring of slots;
+//  * 4 warps do the same for the values, transposed, [d x 64 positions]: a
+//    thread takes 8 positions x 8 neighbouring dims, whose codes are one word
+//    per position, and writes dim 8 dg + j to row j d/8 + dg (then the 8
+//    lanes of a store phase hit 8 different bank groups). The accumulator's
+//    columns come out in that order; a Hadamard transform commutes with such
+//    a permutation of index bits, so the final rotation is done in it;
+//  * one thread per row tile issues tcgen05.mma: S = (Q_hi + Q_lo) K^T into
+//    tensor memory, and O += (P_hi + P_lo) V with P read from tensor memory;
+//  * 4 warps per row tile, one row per thread: scores from tensor memory,
+//    times the key norm, running maximum, weights times value norms as fp16
+//    value + remainder back to tensor memory, over the scores. The maximum
+//    that the weights refer to moves only when it grows by more than 2^8
+//    (exact: sum and accumulator share it), so the accumulator is rescaled
+//    rarely.
+// Scores are double-buffered: the next tile's S is computed while the
+// softmax works on the current one.
+//
+// Per row tile and 64 positions: 4 x 64 x 128 x d multiply-adds (scores and
+// values, each with its remainder: 512 tensor cycles at d = 128), an
+// exponential and about 9 other instructions per score, and the codes'
+// conversion (about 1000 warp instructions) shared by the row tiles.
+#include <climits>
+#include <cmath>
+
+#include "tq_attend_window.cuh"
+#include "tq_umma.cuh"
+
+namespace tq {
+
+constexpr int TW_TP = 64;       // positions of a tile
+constexpr int TW_SLOTS = 4;     // norm slots in flight
+constexpr int TW_TMEM = 512;
+
+// Norms and positions of one tile.
+struct TwSlot {
+  float nk[TW_TP];
+  float nv[TW_TP];   // times the power of two of the tile
+  int blk_t[4];      // first position of each 16-position block (INT_MAX - 64: none)
+  float v_fix;       // this tile's power of two over the previous tile's
+  float v_inv;       // its inverse
+  int pad[2];
+};
+
+template <int D, int KB, int VB>
+struct TwCfg {
+  static constexpr int MT = D == 256 ? 1 : 2;    // row tiles of 128
+  static constexpr int NBUF = D == 256 ? 1 : 2;  // key tiles, value tiles in shared memory
+  static constexpr int SM_WARPS = 4 * MT;
+  static constexpr int WARPS = SM_WARPS + 8 + MT;
+  static constexpr int Q_PART = D * 256;         // [128 rows x d] fp16
+  static constexpr int KV = D * TW_TP * 2;       // [64 x d] fp16
+  static constexpr int K_TAB = (1 << (2 * KB)) * 64;
+  static constexpr int V_TAB = KB == VB ? 0 : (1 << (2 * VB)) * 64;
+  static constexpr int Q0 = 0;
+  static constexpr int K0 = Q0 + 2 * MT * Q_PART;
+  static constexpr int V0 = K0 + NBUF * KV;
+  static constexpr int T0 = V0 + NBUF * KV;
+  static constexpr int N0 = T0 + K_TAB + V_TAB;
+  static constexpr int BAR = N0 + TW_SLOTS * (int)sizeof(TwSlot);
+  static constexpr int BARS = 4 * NBUF + TW_SLOTS + MT * 6;
+  static constexpr int SLOT = BAR + BARS * 8;
+  static constexpr int NEED = SLOT + 16 + 1024;
+  // one CTA per SM also where less shared memory would do: each takes all of
+  // the SM's tensor memory
+  static constexpr int BYTES = NEED < 120 * 1024 ? 120 * 1024 : NEED;
+  static_assert(BYTES <= 232448, "shared memory of a CTA");
+};
+
+// In-register Hadamard transform of 64 values (natural order, no scaling).
+TQ_DEV void wht64(float (&x)[64]) {
+#pragma unroll
+  for (int h = 1; h < 64; h <<= 1)
+#pragma unroll
+    for (int e = 0; e < 64; ++e)
+      if ((e & h) == 0) {
+        const float u = x[e], v = x[e + h];
+        x[e] = u + v;
+        x[e + h] = u - v;
+      }
+}
+
+template <int D, int KB, int VB>
+__global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
+    window_tc_kernel(const __grid_constant__ AwArgs a) {
+  using C = TwCfg<D, KB, VB>;
+  constexpr int MT = C::MT, NBUF = C::NBUF;
+  constexpr int PK = D * KB / 8, PV = D * VB / 8;
+  extern __shared__ uint8_t raw_smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.z;
+  const int split = blockIdx.x / a.hkv, hk = blockIdx.x - split * a.hkv;
+  const AwSeq sq = aw_sequence(a, b, blockIdx.x == 0 && blockIdx.y == 0 && tid == 0);
+  const int rows = sq.n * a.g, r0 = blockIdx.y * (128 * MT);
+  if (r0 >= rows) return;
+
+  // ---- the tiles of this CTA
+  const int r1 = min(r0 + 128 * MT, rows) - 1;
+  const int p_hi = aw_position(sq, r1 / a.g);
+  const AwBlocks bl = aw_blocks(aw_position(sq, r0 / a.g), p_hi, a.window, a.sinks);
+  const int tiles = (bl.n + 3) / 4, share = (tiles + a.n_split - 1) / a.n_split;
+  const int tile0 = split * share, cnt = max(0, min(share, tiles - tile0));
+
+  const uint32_t raw = smem_u32(raw_smem), base = (raw + 1023u) & ~1023u;
+  uint8_t* sm = raw_smem + (base - raw);
+  const uint32_t bar = base + C::BAR;
+  const uint32_t k_full = bar, k_empty = k_full + 8 * NBUF, v_full = k_empty + 8 * NBUF, v_empty = v_full + 8 * NBUF,
+                 n_full = v_empty + 8 * NBUF, s_full = n_full + 8 * TW_SLOTS,  // [MT][2]
+                 p_full = s_full + 16 * MT, o_done = p_full + 16 * MT, mma_end = o_done + 8 * MT;
+  if (tid == 0) {
+    for (int i = 0; i < NBUF; ++i) {
+      mbar_init(k_full + 8 * i, 128);
+      mbar_init(k_empty + 8 * i, MT);
+      mbar_init(v_full + 8 * i, 128);
+      mbar_init(v_empty + 8 * i, MT);
+    }
+    for (int i = 0; i < TW_SLOTS; ++i) mbar_init(n_full + 8 * i, 32);
+    for (int i = 0; i < 2 * MT; ++i) {
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_full + 8 * i, 128);
+    }
+    for (int i = 0; i < MT; ++i) {
+      mbar_init(o_done + 8 * i, 1);
+      mbar_init(mma_end + 8 * i, 1);
+    }
+    fence_mbar_init();
+  }
+  constexpr int MMA_WARP = C::SM_WARPS + 8;
+  if (warp == MMA_WARP) {
+    tmem_alloc(base + C::SLOT, TW_TMEM);
+    tmem_relinquish();
+  }
+  // ---- tables: pairs of codes -> two fp16 levels, 16 copies
+  {
+    uint32_t* t = reinterpret_cast<uint32_t*>(sm + C::T0);
+    for (int e = tid; e < C::K_TAB / 4; e += blockDim.x) {
+      const int f = e >> 4;
+      t[e] = a.k_lev[f & ((1 << KB) - 1)] | (uint32_t)a.k_lev[f >> KB] << 16;
+    }
+    t += C::K_TAB / 4;
+    for (int e = tid; e < C::V_TAB / 4; e += blockDim.x) {
+      const int f = e >> 4;
+      t[e] = a.v_lev[f & ((1 << VB) - 1)] | (uint32_t)a.v_lev[f >> VB] << 16;
+    }
+  }
+  // ---- rotated queries, one row per softmax thread
+  const int mt = warp >> 2;  // softmax warps: row tile
+  const int r_tile = tid & 127, r = r0 + tid;
+  const bool row_ok = warp < C::SM_WARPS && r < rows;
+  const int q_i = row_ok ? r / a.g : 0, q_h = row_ok ? r - q_i * a.g : 0;
+  const int64_t out_row = (sq.q0 + q_i) * a.hq + hk * a.g + q_h;
+  float row_inv = 1.f;
+  if (row_ok) {
+    const uint4* src = reinterpret_cast<const uint4*>(a.q + out_row * D);
+    float ss = 0.f;
+#pragma unroll 4
+    for (int e = 0; e < D / 8; ++e) {
+      const uint4 w = __ldg(src + e);
+      const uint32_t hw[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hw[c]));
+        ss = fmaf(f.x, f.x, fmaf(f.y, f.y, ss));
+      }
+    }
+    // no rotated coordinate exceeds sqrt(d) |q|: that bound is put just below 2^15
+    const float up = aw_pow2_for<14>(sqrtf(ss * (float)D) * a.q_scale, row_inv);
+    const float qs = a.q_scale * up;
+#pragma unroll 1
+    for (int hf = 0; hf < D / 64; ++hf) {
+      float x[64];
+#pragma unroll
+      for (int e = 0; e < 64; ++e) x[e] = 0.f;
+#pragma unroll 1
+      for (int m = 0; m < D / 64; ++m) {
+        const float sg = (__popc(m & hf) & 1) ? -1.f : 1.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint4 w = __ldg(src + 8 * m + e);
+          const uint32_t hw[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t s = hw[c] ^ a.k_sign_h2[32 * m + 4 * e + c];
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&s));
+            x[8 * e + 2 * c] = fmaf(sg, f.x, x[8 * e + 2 * c]);
+            x[8 * e + 2 * c + 1] = fmaf(sg, f.y, x[8 * e + 2 * c + 1]);
+          }
+        }
+      }
+      wht64(x);
+      uint8_t* dst = sm + C::Q0 + 2 * mt * C::Q_PART + hf * 16384 + r_tile * 128;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float u = x[8 * c + 2 * k] * qs, v = x[8 * c + 2 * k + 1] * qs;
+          hi[k] = pack_half2(u, v);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
+          lo[k] = pack_half2(u - f.x, v - f.y);
+        }
+        const int off = (c ^ (r_tile & 7)) << 4;
+        *reinterpret_cast<uint4*>(dst + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(dst + C::Q_PART + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
+  }
+  if (warp < C::SM_WARPS && !row_ok) {  // rows behind the last: scores of 0
+    uint4* dst = reinterpret_cast<uint4*>(sm + C::Q0 + 2 * mt * C::Q_PART + r_tile * 128);
+    for (int e = 0; e < 2 * (D / 64); ++e)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) dst[e * (16384 / 16) + c] = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::SLOT);
+  // row tile t: scores / weights at columns 256 t + {0, 64}, accumulator at 256 t + 128
+  constexpr uint32_t FULL = 0xffffffffu;
+
+  if (warp >= C::SM_WARPS && warp < MMA_WARP) {
+    const bool keys = warp < C::SM_WARPS + 4;
+    const int w4 = (warp - C::SM_WARPS) & 3;
+    if (keys) {
+      // ---- key codes -> K tiles: row 16 w4 + lane % 16, half (lane / 16) of its dims
+      constexpr int HB = PK / 2, HW = HB / 4;
+      const int row = 16 * w4 + (lane & 15), half = lane >> 4;
+      const uint32_t lut = base + C::T0 + (lane & 15) * 4u;
+      uint32_t cw[HW];
+      float nk[2], nv[2];  // of positions lane, lane + 32 (first warp)
+      auto fetch = [&](int i) {
+        const int m = 4 * (tile0 + i) + w4;
+        const int j = aw_block(bl, min(m, bl.n - 1));
+        const int64_t c_row = (aw_block_row(a, b, j) + min(row & 15, sq.ctx - 1 - j * ATT_BLOCK)) * a.hkv + hk;
+        aw_load<HB, HW>(cw, a.k_packed + c_row * PK, half * HB, PK);
+        if (w4 == 0) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int mm = 4 * (tile0 + i) + 2 * h + (lane >> 4);
+            const int jj = aw_block(bl, min(mm, bl.n - 1));
+            const int64_t n_row =
+                (aw_block_row(a, b, jj) + min(lane & 15, sq.ctx - 1 - jj * ATT_BLOCK)) * a.hkv + hk;
+            nk[h] = __ldg(a.k_norms + n_row);
+            nv[h] = __ldg(a.v_norms + n_row);
+          }
+        }
+      };
+      if (cnt > 0) fetch(0);
+      float v_most = 0.f, v_up = 1.f, v_inv = 1.f;
+      for (int i = 0; i < cnt; ++i) {
+        const int buf = i % NBUF;
+        if (i >= NBUF && !__all_sync(FULL, mbar_wait_bounded(k_empty + 8 * buf, ((i / NBUF) - 1) & 1, a.wait_limit))) {
+          if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
+          break;
+        }
+        if (w4 == 0) {
+          TwSlot& s = reinterpret_cast<TwSlot*>(sm + C::N0)[i % TW_SLOTS];
+          float most = 0.f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int mm = 4 * (tile0 + i) + 2 * h + (lane >> 4);
+            const float v = fabsf(nv[h]);
+            if (mm < bl.n && aw_block(bl, mm) * ATT_BLOCK + (lane & 15) <= p_hi && v < INFINITY) most = fmaxf(most, v);
+          }
+#pragma unroll
+          for (int m = 16; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL, most, m));
+          float fix = 1.f;
+          if (most > v_most) {
+            v_most = most;
+            float inv;
+            const float up = aw_pow2_for<5>(most, inv);  // weights reach 2^8: 2^14 in fp16
+            fix = up * v_inv;
+            v_up = up;
+            v_inv = inv;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            s.nk[32 * h + lane] = nk[h];
+            s.nv[32 * h + lane] = nv[h] * v_up;
+          }
+          if (lane < 4) {
+            const int mm = 4 * (tile0 + i) + lane;
+            s.blk_t[lane] = mm < bl.n ? aw_block(bl, mm) * ATT_BLOCK : INT_MAX - 64;
+          }
+          if (lane == 0) {
+            s.v_fix = fix;
+            s.v_inv = v_inv;
+          }
+          mbar_arrive(n_full + 8 * (i % TW_SLOTS));
+        }
+        uint8_t* dst = sm + C::K0 + buf * C::KV + row * 128;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {  // 8 dims each
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = lds32(aw_bits<2 * KB>(cw, (4 * c + k) * 2 * KB) * 64u + lut);
+          const int chunk = half * (D / 16) + c;  // 16-byte chunk of the row: atom chunk / 8
+          *reinterpret_cast<uint4*>(dst + (chunk >> 3) * (TW_TP * 128) + (((chunk & 7) ^ (row & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (i + 1 < cnt) fetch(i + 1);
+        fence_proxy_async_smem();
+        mbar_arrive(k_full + 8 * buf);
+      }
+    } else {
+      // ---- value codes -> V tiles: positions 8 pg ..., dims 8 dg ... of a thread
+      constexpr int DG = D / 8, PASS = D == 256 ? 2 : 1;  // 128 threads cover 128 / DG groups of 8 positions
+      const int t = w4 * 32 + lane, dg = t % DG, pg0 = t / DG;
+      const bool on = D > 64 || pg0 < 8;
+      const uint32_t lut = base + C::T0 + C::K_TAB * (KB == VB ? 0 : 1) + (lane & 15) * 4u;
+      uint32_t vw[PASS][8];
+      auto fetch = [&](int i) {
+#pragma unroll
+        for (int q = 0; q < PASS; ++q) {
+          const int pg = pg0 + q * (128 / DG);
+          const int m = 4 * (tile0 + i) + (pg >> 1);
+          const int j = aw_block(bl, min(m, bl.n - 1));
+          const int64_t row0 = aw_block_row(a, b, j);
+          const int most = sq.ctx - 1 - j * ATT_BLOCK;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint32_t w[1];
+            const int64_t v_row = (row0 + min(8 * (pg & 1) + k, most)) * a.hkv + hk;
+            aw_load<VB, 1>(w, a.v_packed + v_row * PV, dg * VB, PV);
+            vw[q][k] = w[0];
+          }
+        }
+      };
+      if (cnt > 0 && on) fetch(0);
+      for (int i = 0; i < cnt; ++i) {
+        const int buf = i % NBUF;
+        if (i >= NBUF && !__all_sync(FULL, mbar_wait_bounded(v_empty + 8 * buf, ((i / NBUF) - 1) & 1, a.wait_limit))) {
+          if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
+          break;
+        }
+        if (on) {
+#pragma unroll
+          for (int q = 0; q < PASS; ++q) {
+            const int pg = pg0 + q * (128 / DG);
+            uint8_t* dst = sm + C::V0 + buf * C::KV + dg * 128 + ((pg ^ (dg & 7)) << 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // dims 8 dg + 2 j, + 1
+              uint32_t l[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) l[k] = lds32(((vw[q][k] >> (2 * VB * j)) & ((1u << 2 * VB) - 1u)) * 64u + lut);
+              uint32_t e[4], o[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                e[k] = __byte_perm(l[2 * k], l[2 * k + 1], 0x5410);
+                o[k] = __byte_perm(l[2 * k], l[2 * k + 1], 0x7632);
+              }
+              *reinterpret_cast<uint4*>(dst + (2 * j) * DG * 128) = make_uint4(e[0], e[1], e[2], e[3]);
+              *reinterpret_cast<uint4*>(dst + (2 * j + 1) * DG * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+          if (i + 1 < cnt) fetch(i + 1);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(v_full + 8 * buf);
+      }
+    }
+  } else if (warp >= MMA_WARP) {
+    // ---- MMA issuer of row tile t
+    if (lane == 0) {
+      const int t = warp - MMA_WARP;
+      constexpr uint32_t ID_S = umma_idesc_f16(128, TW_TP), ID_O = umma_idesc_f16(128, D);
+      const uint32_t s0 = tmem + 256u * t, o0 = s0 + 128u;
+      const uint64_t q_desc = umma_desc_sw128(base + C::Q0 + 2 * t * C::Q_PART);
+      const uint64_t k_desc = umma_desc_sw128(base + C::K0), v_desc = umma_desc_sw128(base + C::V0);
+      bool ok = true;
+      for (int i = 0; i <= cnt && ok; ++i) {
+        if (i < cnt) {
+          const int buf = i % NBUF;
+          ok = mbar_wait_bounded(k_full + 8 * buf, (i / NBUF) & 1, a.wait_limit);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t s = s0 + 64u * (i & 1);
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+              umma_f16(s, q_desc + ((part * C::Q_PART + (ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                       k_desc + ((buf * C::KV + (ks >> 2) * (TW_TP * 128) + (ks & 3) * 32) >> 4), ID_S,
+                       part + ks > 0);
+          umma_commit(s_full + 16 * t + 8 * (i & 1));
+          umma_commit(k_empty + 8 * buf);
+        }
+        if (i > 0) {
+          const int j = i - 1, buf = j % NBUF;
+          ok = mbar_wait_bounded(v_full + 8 * buf, (j / NBUF) & 1, a.wait_limit) &&
+               mbar_wait_bounded(p_full + 16 * t + 8 * (j & 1), (j >> 1) & 1, a.wait_limit);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t p = s0 + 64u * (j & 1);
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int ks = 0; ks < TW_TP / 16; ++ks)
+              umma_f16_ts(o0, p + (uint32_t)(32 * part + 8 * ks), v_desc + ((buf * C::KV + ks * 32) >> 4), ID_O,
+                          part + ks > 0 || j > 0);
+          umma_commit(o_done + 8 * t);
+          umma_commit(v_empty + 8 * buf);
+        }
+      }
+      if (!ok) record_error(a.err, TQ_DEVERR_TIMEOUT);
+      umma_commit(mma_end + 8 * t);
+      if (!mbar_wait_bounded(mma_end + 8 * t, 0, a.wait_limit)) record_error(a.err, TQ_DEVERR_TIMEOUT);
+    }
+  } else {
+    // ---- softmax of one row per thread
+    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t s0 = tmem + 256u * mt + lane_base, o0 = s0 + 128u;
+    const int rw0 = r0 + 32 * warp, rw1 = min(rw0 + 31, rows - 1);  // rows of this warp
+    const bool any_row = rw0 < rows;
+    const int pw_lo = any_row ? aw_position(sq, rw0 / a.g) : -1, pw_hi = any_row ? aw_position(sq, rw1 / a.g) : -1;
+    const int p_row = row_ok ? aw_position(sq, q_i) : pw_hi;
+    float m_ref = -INFINITY, l_sum = 0.f, v_inv = 1.f;
+    bool ok = true;
+    for (int i = 0; i < cnt; ++i) {
+      ok = mbar_wait_bounded(s_full + 16 * mt + 8 * (i & 1), (i >> 1) & 1, a.wait_limit) &&
+           mbar_wait_bounded(n_full + 8 * (i % TW_SLOTS), (i / TW_SLOTS) & 1, a.wait_limit);
+      ok = __all_sync(FULL, ok);
+      if (!ok) {
+        if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t sp = s0 + 64u * (i & 1);
+      if (any_row) {
+        const TwSlot& slot = reinterpret_cast<const TwSlot*>(sm + C::N0)[i % TW_SLOTS];
+        float x[64];
+        {
+          uint32_t u[32], v[32];
+          tmem_ld32(sp, u);
+          tmem_ld32(sp + 32u, v);
+          tmem_wait_ld();
+          tmem_regs_after_wait(u);
+          tmem_regs_after_wait(v);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(u[c]), x[c + 32] = __uint_as_float(v[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          const float4 n = *reinterpret_cast<const float4*>(slot.nk + c);
+          const f2 u = mul2(make_float2(x[c], x[c + 1]), make_float2(n.x, n.y));
+          const f2 v = mul2(make_float2(x[c + 2], x[c + 3]), make_float2(n.z, n.w));
+          x[c] = u.x, x[c + 1] = u.y, x[c + 2] = v.x, x[c + 3] = v.y;
+        }
+        uint32_t hidden = 0;  // blocks with masked positions for this warp's rows
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int t0 = slot.blk_t[h], t1 = t0 + ATT_BLOCK - 1;
+          if (t1 <= pw_lo && (t1 < a.sinks || t0 > pw_hi - a.window)) continue;
+          hidden |= 1u << h;
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (!aw_visible(t0 + c, p_row, a.window, a.sinks)) x[16 * h + c] = -INFINITY;
+        }
+        float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+#pragma unroll
+        for (int c = 4; c < 64; c += 4) {
+          mx0 = fmaxf(mx0, x[c]);
+          mx1 = fmaxf(mx1, x[c + 1]);
+          mx2 = fmaxf(mx2, x[c + 2]);
+          mx3 = fmaxf(mx3, x[c + 3]);
+        }
+        const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * row_inv;
+        // the reference follows the maximum when it is exceeded by 2^8
+        const bool move = mx > m_ref + 8.0f || (m_ref == -INFINITY && mx != -INFINITY);
+        const float v_fix = slot.v_fix;
+        v_inv = slot.v_inv;
+        float fix = v_fix;
+        if (move) {
+          const float f = aw_exp2(m_ref - mx);  // 0 from -inf
+          l_sum *= f;
+          fix *= f;
+          m_ref = mx;
+        }
+        if (i > 0 && __any_sync(FULL, move || v_fix != 1.0f)) {
+          // the previous product must be in the accumulator before it is rescaled
+          const bool done = __all_sync(FULL, mbar_wait_bounded(o_done + 8 * mt, (i - 1) & 1, a.wait_limit));
+          if (!done) {
+            if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            uint32_t u[16];
+            tmem_ld16(o0 + (uint32_t)c0, u);
+            tmem_wait_ld();
+            tmem_regs_after_wait(u);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * fix);
+            tmem_st16(o0 + (uint32_t)c0, u);
+          }
+        }
+        const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int c0 = 0; c0 < 64; c0 += 32) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 n = *reinterpret_cast<const float4*>(slot.nv + c0 + c);
+            const float nn[4] = {n.x, n.y, n.z, n.w};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int e = c0 + c + 2 * k;
+              const f2 z = fma2(make_float2(x[e], x[e + 1]), make_float2(row_inv, row_inv), make_float2(-ref, -ref));
+              const f2 p = make_float2(aw_exp2(z.x), aw_exp2(z.y));
+              sum0 += p.x;
+              sum1 += p.y;
+              f2 w = mul2(p, make_float2(nn[2 * k], nn[2 * k + 1]));
+              if (hidden >> (e / 16) & 1u) {  // a masked norm may be anything
+                if (x[e] == -INFINITY) w.x = 0.f;
+                if (x[e + 1] == -INFINITY) w.y = 0.f;
+              }
+              const uint32_t h2 = pack_half2(w.x, w.y);
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+              hi[c / 2 + k] = h2;
+              lo[c / 2 + k] = pack_half2(w.x - f.x, w.y - f.y);
+            }
+          }
+          tmem_st16(sp + (uint32_t)(c0 / 2), hi);
+          tmem_st16(sp + 32u + (uint32_t)(c0 / 2), lo);
+        }
+        l_sum += sum0 + sum1;
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      mbar_arrive(p_full + 16 * mt + 8 * (i & 1));
+    }
+    // ---- results
+    if (ok && cnt > 0) {
+      ok = __all_sync(FULL, mbar_wait_bounded(o_done + 8 * mt, (cnt - 1) & 1, a.wait_limit));
+      if (!ok && lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
+      tc_fence_after();
+    }
+    if (any_row && ok) {
+      const bool empty = cnt == 0 || m_ref == -INFINITY;
+      const int64_t idx = out_row * a.n_split + split;
+      if (a.n_split > 1 && row_ok) {
+        a.ws_m[idx] = empty && l_sum == 0.f ? -INFINITY : m_ref;
+        a.ws_l[idx] = l_sum;
+      }
+      const float scale = a.n_split > 1 ? v_inv : (l_sum > 0.f ? v_inv * a.o_scale / l_sum : (l_sum == l_sum ? 0.f : l_sum));
+#pragma unroll 1
+      for (int hf = 0; hf < D / 64; ++hf) {
+        float x[64];
+#pragma unroll
+        for (int e = 0; e < 64; ++e) x[e] = 0.f;
+        if (cnt > 0) {
+#pragma unroll 1
+          for (int m = a.n_split > 1 ? hf : 0; m < (a.n_split > 1 ? hf + 1 : D / 64); ++m) {
+            const float sg = a.n_split > 1 || !(__popc(m & hf) & 1) ? 1.f : -1.f;
+#pragma unroll
+            for (int c0 = 0; c0 < 64; c0 += 16) {
+              uint32_t u[16];
+              tmem_ld16(o0 + (uint32_t)(64 * m + c0), u);
+              tmem_wait_ld();
+              tmem_regs_after_wait(u);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) x[c0 + c] = fmaf(sg, __uint_as_float(u[c]), x[c0 + c]);
+            }
+          }
+        }
+        if (a.n_split == 1) wht64(x);
+        // column 64 hf + e is dim 8 (e % DG) + JN hf + e / DG: JN neighbouring dims per group
+        constexpr int DG = D / 8, JN = 64 / DG;
+#pragma unroll
+        for (int dg = 0; dg < DG && row_ok; ++dg) {
+          float y[JN];
+#pragma unroll
+          for (int j = 0; j < JN; ++j) y[j] = x[j * DG + dg] * scale;
+          const int dim = 8 * dg + JN * hf;
+          if (a.n_split > 1) {
+            if (!empty) {
+              float2* dst = reinterpret_cast<float2*>(a.ws_acc + idx * D + dim);
+#pragma unroll
+              for (int j = 0; j < JN; j += 2) dst[j / 2] = make_float2(y[j], y[j + 1]);
+            }
+          } else {
+            uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + out_row * D + dim);
+#pragma unroll
+            for (int j = 0; j < JN; j += 2)
+              dst[j / 2] = empty && l_sum == 0.f ? 0u : pack_half2(y[j], y[j + 1]) ^ a.v_sign_h2[(dim + j) / 2];
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    __syncwarp();
+    tmem_dealloc(tmem, TW_TMEM);
+  }
+}
+
+template <int D, int KB, int VB>
+static cudaError_t launch_tc_t(const AwArgs& a, cudaStream_t st) {
+  using C = TwCfg<D, KB, VB>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(window_tc_kernel<D, KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+  if (e != cudaSuccess) return e;
+  const int64_t gx = (int64_t)a.n_split * a.hkv, gy = ((int64_t)a.max_q * a.g + 128 * C::MT - 1) / (128 * C::MT);
+  if (gx > 0x7fffffff || gy > 65535) return cudaErrorNotSupported;
+  window_tc_kernel<D, KB, VB><<<dim3((unsigned)gx, (unsigned)gy, a.B), C::WARPS * 32, C::BYTES, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t launch_tc_d(const AwArgs& a, int kb, int vb, cudaStream_t st) {
+#define TQ_TW_CASE(KB_, VB_) \
+  if (kb == KB_ && vb == VB_) return launch_tc_t<D, KB_, VB_>(a, st);
+  TQ_TW_CASE(2, 2) TQ_TW_CASE(2, 3) TQ_TW_CASE(2, 4) TQ_TW_CASE(3, 2) TQ_TW_CASE(3, 3) TQ_TW_CASE(3, 4)
+  TQ_TW_CASE(4, 2) TQ_TW_CASE(4, 3) TQ_TW_CASE(4, 4)
+#undef TQ_TW_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace tq
+
+using namespace tq;
+
+int tq_window_tc_rows(int d) { return d == 256 ? 128 : 256; }
+
+cudaError_t tq_launch_window_tc(const AwArgs& a, int d, int kb, int vb, cudaStream_t st) {
+  if (d == 64) return launch_tc_d<64>(a, kb, vb, st);
+  if (d == 128) return launch_tc_d<128>(a, kb, vb, st);
+  return launch_tc_d<256>(a, kb, vb, st);
+}
