@@ -59,7 +59,14 @@ struct TwCfg {
   static constexpr int MT = D == 256 ? 1 : 2;    // row tiles of 128
   static constexpr int NBUF = D == 256 ? 1 : 2;  // key tiles, value tiles in shared memory
   static constexpr int SM_WARPS = 4 * MT;
-  static constexpr int WARPS = SM_WARPS + 8 + MT;
+  // softmax, conversion and issuing warpgroups (of the last, MT warps work)
+  static constexpr int WARPS = SM_WARPS + 8 + 4;
+  // registers of a thread by role: a softmax row (64 scores and their packed
+  // weights) needs more than the launch's share of the register file. Per
+  // scheduler MT R_SM + 2 R_CV + R_MMA is the MT + 3 launched warps' share
+  // (96 at MT = 2, 128 at MT = 1) or less.
+  static constexpr int R_SM = MT == 2 ? 144 : 160, R_CV = MT == 2 ? 64 : 120, R_MMA = MT == 2 ? 64 : 96;
+  static_assert(MT * R_SM + 2 * R_CV + R_MMA <= (MT + 3) * (MT == 2 ? 96 : 128), "register shares");
   static constexpr int Q_PART = D * 256;         // [128 rows x d] fp16
   static constexpr int KV = D * TW_TP * 2;       // [64 x d] fp16
   static constexpr int K_TAB = (1 << (2 * KB)) * 64;
@@ -70,7 +77,7 @@ struct TwCfg {
   static constexpr int T0 = V0 + NBUF * KV;
   static constexpr int N0 = T0 + K_TAB + V_TAB;
   static constexpr int BAR = N0 + TW_SLOTS * (int)sizeof(TwSlot);
-  static constexpr int BARS = 4 * NBUF + TW_SLOTS + MT * 6;
+  static constexpr int BARS = 4 * NBUF + TW_SLOTS + MT * 8;
   static constexpr int SLOT = BAR + BARS * 8;
   static constexpr int NEED = SLOT + 16 + 1024;
   // one CTA per SM also where less shared memory would do: each takes all of
@@ -90,6 +97,15 @@ TQ_DEV void wht64(float (&x)[64]) {
         x[e] = u + v;
         x[e + h] = u - v;
       }
+}
+
+template <int N>
+TQ_DEV void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+TQ_DEV void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <int D, int KB, int VB>
@@ -118,7 +134,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
   const uint32_t bar = base + C::BAR;
   const uint32_t k_full = bar, k_empty = k_full + 8 * NBUF, v_full = k_empty + 8 * NBUF, v_empty = v_full + 8 * NBUF,
                  n_full = v_empty + 8 * NBUF, s_full = n_full + 8 * TW_SLOTS,  // [MT][2]
-                 p_full = s_full + 16 * MT, o_done = p_full + 16 * MT, mma_end = o_done + 8 * MT;
+                 p_full = s_full + 16 * MT, o_done = p_full + 16 * MT, mma_end = o_done + 16 * MT, q_full = mma_end + 8 * MT;
   if (tid == 0) {
     for (int i = 0; i < NBUF; ++i) {
       mbar_init(k_full + 8 * i, 128);
@@ -130,10 +146,11 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
     for (int i = 0; i < 2 * MT; ++i) {
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 128);
+      mbar_init(o_done + 8 * i, 1);
     }
     for (int i = 0; i < MT; ++i) {
-      mbar_init(o_done + 8 * i, 1);
       mbar_init(mma_end + 8 * i, 1);
+      mbar_init(q_full + 8 * i, 128);
     }
     fence_mbar_init();
   }
@@ -155,75 +172,6 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
       t[e] = a.v_lev[f & ((1 << VB) - 1)] | (uint32_t)a.v_lev[f >> VB] << 16;
     }
   }
-  // ---- rotated queries, one row per softmax thread
-  const int mt = warp >> 2;  // softmax warps: row tile
-  const int r_tile = tid & 127, r = r0 + tid;
-  const bool row_ok = warp < C::SM_WARPS && r < rows;
-  const int q_i = row_ok ? r / a.g : 0, q_h = row_ok ? r - q_i * a.g : 0;
-  const int64_t out_row = (sq.q0 + q_i) * a.hq + hk * a.g + q_h;
-  float row_inv = 1.f;
-  if (row_ok) {
-    const uint4* src = reinterpret_cast<const uint4*>(a.q + out_row * D);
-    float ss = 0.f;
-#pragma unroll 4
-    for (int e = 0; e < D / 8; ++e) {
-      const uint4 w = __ldg(src + e);
-      const uint32_t hw[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hw[c]));
-        ss = fmaf(f.x, f.x, fmaf(f.y, f.y, ss));
-      }
-    }
-    // no rotated coordinate exceeds sqrt(d) |q|: that bound is put just below 2^15
-    const float up = aw_pow2_for<14>(sqrtf(ss * (float)D) * a.q_scale, row_inv);
-    const float qs = a.q_scale * up;
-#pragma unroll 1
-    for (int hf = 0; hf < D / 64; ++hf) {
-      float x[64];
-#pragma unroll
-      for (int e = 0; e < 64; ++e) x[e] = 0.f;
-#pragma unroll 1
-      for (int m = 0; m < D / 64; ++m) {
-        const float sg = (__popc(m & hf) & 1) ? -1.f : 1.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint4 w = __ldg(src + 8 * m + e);
-          const uint32_t hw[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t s = hw[c] ^ a.k_sign_h2[32 * m + 4 * e + c];
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&s));
-            x[8 * e + 2 * c] = fmaf(sg, f.x, x[8 * e + 2 * c]);
-            x[8 * e + 2 * c + 1] = fmaf(sg, f.y, x[8 * e + 2 * c + 1]);
-          }
-        }
-      }
-      wht64(x);
-      uint8_t* dst = sm + C::Q0 + 2 * mt * C::Q_PART + hf * 16384 + r_tile * 128;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float u = x[8 * c + 2 * k] * qs, v = x[8 * c + 2 * k + 1] * qs;
-          hi[k] = pack_half2(u, v);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
-          lo[k] = pack_half2(u - f.x, v - f.y);
-        }
-        const int off = (c ^ (r_tile & 7)) << 4;
-        *reinterpret_cast<uint4*>(dst + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(dst + C::Q_PART + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-    }
-  }
-  if (warp < C::SM_WARPS && !row_ok) {  // rows behind the last: scores of 0
-    uint4* dst = reinterpret_cast<uint4*>(sm + C::Q0 + 2 * mt * C::Q_PART + r_tile * 128);
-    for (int e = 0; e < 2 * (D / 64); ++e)
-#pragma unroll
-      for (int c = 0; c < 8; ++c) dst[e * (16384 / 16) + c] = make_uint4(0, 0, 0, 0);
-  }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -232,6 +180,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
   constexpr uint32_t FULL = 0xffffffffu;
 
   if (warp >= C::SM_WARPS && warp < MMA_WARP) {
+    regs_down<C::R_CV>();
     const bool keys = warp < C::SM_WARPS + 4;
     const int w4 = (warp - C::SM_WARPS) & 3;
     if (keys) {
@@ -374,13 +323,14 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
     }
   } else if (warp >= MMA_WARP) {
     // ---- MMA issuer of row tile t
-    if (lane == 0) {
-      const int t = warp - MMA_WARP;
+    regs_down<C::R_MMA>();
+    const int t = warp - MMA_WARP;
+    if (t < MT && lane == 0) {
       constexpr uint32_t ID_S = umma_idesc_f16(128, TW_TP), ID_O = umma_idesc_f16(128, D);
       const uint32_t s0 = tmem + 256u * t, o0 = s0 + 128u;
       const uint64_t q_desc = umma_desc_sw128(base + C::Q0 + 2 * t * C::Q_PART);
       const uint64_t k_desc = umma_desc_sw128(base + C::K0), v_desc = umma_desc_sw128(base + C::V0);
-      bool ok = true;
+      bool ok = mbar_wait_bounded(q_full + 8 * t, 0, a.wait_limit);
       for (int i = 0; i <= cnt && ok; ++i) {
         if (i < cnt) {
           const int buf = i % NBUF;
@@ -411,7 +361,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
             for (int ks = 0; ks < TW_TP / 16; ++ks)
               umma_f16_ts(o0, p + (uint32_t)(32 * part + 8 * ks), v_desc + ((buf * C::KV + ks * 32) >> 4), ID_O,
                           part + ks > 0 || j > 0);
-          umma_commit(o_done + 8 * t);
+          umma_commit(o_done + 16 * t + 8 * (j & 1));
           umma_commit(v_empty + 8 * buf);
         }
       }
@@ -420,6 +370,77 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
       if (!mbar_wait_bounded(mma_end + 8 * t, 0, a.wait_limit)) record_error(a.err, TQ_DEVERR_TIMEOUT);
     }
   } else {
+    regs_up<C::R_SM>();
+    // ---- rotated queries, one row per softmax thread
+    const int mt = warp >> 2;  // row tile
+    const int r_tile = tid & 127, r = r0 + tid;
+    const bool row_ok = r < rows;
+    const int q_i = row_ok ? r / a.g : 0, q_h = row_ok ? r - q_i * a.g : 0;
+    const int64_t out_row = (sq.q0 + q_i) * a.hq + hk * a.g + q_h;
+    float row_inv = 1.f;
+    if (row_ok) {
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + out_row * D);
+      float ss = 0.f;
+  #pragma unroll 4
+      for (int e = 0; e < D / 8; ++e) {
+        const uint4 w = __ldg(src + e);
+        const uint32_t hw[4] = {w.x, w.y, w.z, w.w};
+  #pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hw[c]));
+          ss = fmaf(f.x, f.x, fmaf(f.y, f.y, ss));
+        }
+      }
+      // no rotated coordinate exceeds sqrt(d) |q|: that bound is put just below 2^15
+      const float up = aw_pow2_for<14>(sqrtf(ss * (float)D) * a.q_scale, row_inv);
+      const float qs = a.q_scale * up;
+  #pragma unroll 1
+      for (int hf = 0; hf < D / 64; ++hf) {
+        float x[64];
+  #pragma unroll
+        for (int e = 0; e < 64; ++e) x[e] = 0.f;
+  #pragma unroll 1
+        for (int m = 0; m < D / 64; ++m) {
+          const float sg = (__popc(m & hf) & 1) ? -1.f : 1.f;
+  #pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint4 w = __ldg(src + 8 * m + e);
+            const uint32_t hw[4] = {w.x, w.y, w.z, w.w};
+  #pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t s = hw[c] ^ a.k_sign_h2[32 * m + 4 * e + c];
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&s));
+              x[8 * e + 2 * c] = fmaf(sg, f.x, x[8 * e + 2 * c]);
+              x[8 * e + 2 * c + 1] = fmaf(sg, f.y, x[8 * e + 2 * c + 1]);
+            }
+          }
+        }
+        wht64(x);
+        uint8_t* dst = sm + C::Q0 + 2 * mt * C::Q_PART + hf * 16384 + r_tile * 128;
+  #pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t hi[4], lo[4];
+  #pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float u = x[8 * c + 2 * k] * qs, v = x[8 * c + 2 * k + 1] * qs;
+            hi[k] = pack_half2(u, v);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
+            lo[k] = pack_half2(u - f.x, v - f.y);
+          }
+          const int off = (c ^ (r_tile & 7)) << 4;
+          *reinterpret_cast<uint4*>(dst + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(dst + C::Q_PART + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+    }
+    if (!row_ok) {  // rows behind the last: scores of 0
+      uint4* dst = reinterpret_cast<uint4*>(sm + C::Q0 + 2 * mt * C::Q_PART + r_tile * 128);
+      for (int e = 0; e < 2 * (D / 64); ++e)
+  #pragma unroll
+        for (int c = 0; c < 8; ++c) dst[e * (16384 / 16) + c] = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(q_full + 8 * mt);
     // ---- softmax of one row per thread
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s0 = tmem + 256u * mt + lane_base, o0 = s0 + 128u;
@@ -490,8 +511,12 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
           m_ref = mx;
         }
         if (i > 0 && __any_sync(FULL, move || v_fix != 1.0f)) {
-          // the previous product must be in the accumulator before it is rescaled
-          const bool done = __all_sync(FULL, mbar_wait_bounded(o_done + 8 * mt, (i - 1) & 1, a.wait_limit));
+          // the previous product must be in the accumulator before it is
+          // rescaled. (Even and odd tiles have barriers of their own: a wait
+          // may be the first in many tiles, and this one's earlier phases
+          // ended before the scores of tile i - 1 were complete.)
+          const bool done = __all_sync(
+              FULL, mbar_wait_bounded(o_done + 16 * mt + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, a.wait_limit));
           if (!done) {
             if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
             ok = false;
@@ -547,7 +572,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
     }
     // ---- results
     if (ok && cnt > 0) {
-      ok = __all_sync(FULL, mbar_wait_bounded(o_done + 8 * mt, (cnt - 1) & 1, a.wait_limit));
+      ok = __all_sync(FULL, mbar_wait_bounded(mma_end + 8 * mt, 0, a.wait_limit));  // every product is done
       if (!ok && lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
       tc_fence_after();
     }
