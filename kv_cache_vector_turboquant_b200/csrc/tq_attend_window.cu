@@ -440,7 +440,11 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_consta
   const float* ms = a.ws_m + row * a.n_split;
   const float* ls = a.ws_l + row * a.n_split;
   float M = -INFINITY;
-  for (int s = lane; s < a.n_split; s += 32) M = fmaxf(M, ms[s]);
+  bool bad = false;  // a NaN score leaves a NaN sum, whatever its split's maximum
+  for (int s = lane; s < a.n_split; s += 32) {
+    M = fmaxf(M, ms[s]);
+    bad = bad || ls[s] != ls[s];
+  }
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
   float x[E], l = 0.f;
@@ -470,7 +474,8 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_consta
   }
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) l += __shfl_xor_sync(0xffffffffu, l, m);
-  const float inv = l > 0.f ? a.o_scale / l : 0.f;
+  float inv = l > 0.f ? a.o_scale / l : 0.f;
+  if (__any_sync(0xffffffffu, bad)) inv = __int_as_float(0x7fc00000);
 #pragma unroll
   for (int h = 1; h < E; h <<= 1)
 #pragma unroll

@@ -98,16 +98,22 @@ TQ_DEV AwBlocks aw_blocks(int p_lo, int p_hi, int window, int sinks) {
 }
 TQ_DEV int aw_block(const AwBlocks& r, int m) { return m < r.n_sink ? m : r.w0 + (m - r.n_sink); }
 
-// Cache row (all kv heads) of the first position of block j of sequence b.
-TQ_DEV int64_t aw_block_row(const AwArgs& a, int b, int j) {
-  if (a.block_tables == nullptr) return (int64_t)b * a.s_max + (int64_t)j * ATT_BLOCK;
-  int64_t page = __ldg(a.block_tables + (int64_t)b * a.max_blocks + j);
+// Cache row (all kv heads) of the first position of block j of sequence b, in
+// two steps so that the table entry can be loaded ahead of its use: the entry
+// (j itself in contiguous caches) and its row.
+TQ_DEV int aw_block_entry(const AwArgs& a, int b, int j) {
+  return a.block_tables == nullptr ? j : __ldg(a.block_tables + (int64_t)b * a.max_blocks + j);
+}
+TQ_DEV int64_t aw_entry_row(const AwArgs& a, int b, int entry) {
+  if (a.block_tables == nullptr) return (int64_t)b * a.s_max + (int64_t)entry * ATT_BLOCK;
+  int64_t page = entry;
   if (page < 0 || page >= a.num_blocks) {
     record_error(a.err, TQ_DEVERR_BLOCK_RANGE);
     page = page < 0 ? 0 : a.num_blocks - 1;
   }
   return page * ATT_BLOCK;
 }
+TQ_DEV int64_t aw_block_row(const AwArgs& a, int b, int j) { return aw_entry_row(a, b, aw_block_entry(a, b, j)); }
 
 TQ_DEV float aw_exp2(float x) {
   float y;

@@ -49,15 +49,17 @@ struct TwSlot {
   float nk[TW_TP];
   float nv[TW_TP];   // times the power of two of the tile
   int blk_t[4];      // first position of each 16-position block (INT_MAX - 64: none)
+  int t_min, t_max;  // first and last position
   float v_fix;       // this tile's power of two over the previous tile's
   float v_inv;       // its inverse
-  int pad[2];
+  int odd;           // some norm is infinite or NaN
+  int pad[3];
 };
 
 template <int D, int KB, int VB>
 struct TwCfg {
   static constexpr int MT = D == 256 ? 1 : 2;    // row tiles of 128
-  static constexpr int NBUF = D == 256 ? 1 : 2;  // key tiles, value tiles in shared memory
+  static constexpr int NBUF = D == 256 ? 1 : 2;  // key operands, value operands in shared memory
   static constexpr int SM_WARPS = 4 * MT;
   // softmax, conversion and issuing warpgroups (of the last, MT warps work)
   static constexpr int WARPS = SM_WARPS + 8 + 4;
@@ -69,8 +71,8 @@ struct TwCfg {
   static_assert(MT * R_SM + 2 * R_CV + R_MMA <= (MT + 3) * (MT == 2 ? 96 : 128), "register shares");
   static constexpr int Q_PART = D * 256;         // [128 rows x d] fp16
   static constexpr int KV = D * TW_TP * 2;       // [64 x d] fp16
-  static constexpr int K_TAB = (1 << (2 * KB)) * 64;
-  static constexpr int V_TAB = KB == VB ? 0 : (1 << (2 * VB)) * 64;
+  static constexpr int K_TAB = KB == 2 ? 0 : (1 << (2 * KB)) * 64;
+  static constexpr int V_TAB = VB == 2 || KB == VB ? 0 : (1 << (2 * VB)) * 64;
   static constexpr int Q0 = 0;
   static constexpr int K0 = Q0 + 2 * MT * Q_PART;
   static constexpr int V0 = K0 + NBUF * KV;
@@ -97,6 +99,54 @@ TQ_DEV void wht64(float (&x)[64]) {
         x[e] = u + v;
         x[e + h] = u - v;
       }
+}
+
+// fp16 levels of the two 2-bit codes at bits 0 and 8 of x (other bits ignored):
+// a byte permute of the four levels in two words, code c taking bytes 2c, 2c + 1.
+TQ_DEV uint32_t tw_levels2(uint32_t x, uint32_t lo, uint32_t hi) {
+  return __byte_perm(lo, hi, (x & 0x0303u) * 0x22u + 0x1010u);
+}
+
+TQ_DEV float tw_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Weights 2^(x row_inv - ref) of a row's 64 scores; returns their sum and
+// stores weight x value norm as fp16 value (columns 0-31 from `col`) and
+// remainder (32-63).
+template <bool CHECK>
+TQ_DEV float tw_weights(const float (&x)[64], const float* nv, float row_inv, float ref, uint32_t col) {
+  f2 sum = make_float2(0.f, 0.f);
+  const f2 scale = make_float2(row_inv, row_inv), shift = make_float2(-ref, -ref);
+#pragma unroll
+  for (int c0 = 0; c0 < 64; c0 += 32) {
+    uint32_t hi[16], lo[16];
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+      const float4 n4 = *reinterpret_cast<const float4*>(nv + c0 + c);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int e = c0 + c + 2 * k;
+        const f2 z = fma2(make_float2(x[e], x[e + 1]), scale, shift);
+        const f2 p = make_float2(aw_exp2(z.x), aw_exp2(z.y));
+        sum = add2(sum, p);
+        f2 w = mul2(p, k ? make_float2(n4.z, n4.w) : make_float2(n4.x, n4.y));
+        if (CHECK) {
+          if (x[e] == -INFINITY) w.x = 0.f;
+          if (x[e + 1] == -INFINITY) w.y = 0.f;
+        }
+        const uint32_t h2 = pack_half2(w.x, w.y);
+        const f2 r = sub2(w, __half22float2(*reinterpret_cast<const __half2*>(&h2)));
+        hi[c / 2 + k] = h2;
+        lo[c / 2 + k] = pack_half2(r.x, r.y);
+      }
+    }
+    tmem_st16(col + (uint32_t)(c0 / 2), hi);
+    tmem_st16(col + 32u + (uint32_t)(c0 / 2), lo);
+  }
+  return sum.x + sum.y;
 }
 
 template <int N>
@@ -137,7 +187,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
                  p_full = s_full + 16 * MT, o_done = p_full + 16 * MT, mma_end = o_done + 16 * MT, q_full = mma_end + 8 * MT;
   if (tid == 0) {
     for (int i = 0; i < NBUF; ++i) {
-      mbar_init(k_full + 8 * i, 128);
+      mbar_init(k_full + 8 * i, 128 + 32);  // the key warps and the norm warp
       mbar_init(k_empty + 8 * i, MT);
       mbar_init(v_full + 8 * i, 128);
       mbar_init(v_empty + 8 * i, MT);
@@ -172,6 +222,19 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
       t[e] = a.v_lev[f & ((1 << VB) - 1)] | (uint32_t)a.v_lev[f >> VB] << 16;
     }
   }
+  // ---- query rows, as they are, into the space of the key and value operands
+  // (row r at r x 2 d bytes, 16-byte chunks swizzled within 128 bytes)
+  static_assert(C::NBUF * 2 * C::KV == 128 * MT * D * 2, "room for the raw query rows");
+  {
+    constexpr int CH = D / 8;  // chunks of a row
+    const int n_rows = min(128 * MT, rows - r0);
+    for (int e = tid; e < n_rows * CH; e += C::WARPS * 32) {
+      const int rr = e / CH, c = e % CH;
+      const int i = (r0 + rr) / a.g, h = r0 + rr - i * a.g;
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(a.q + ((sq.q0 + i) * a.hq + hk * a.g + h) * D) + c);
+      *reinterpret_cast<uint4*>(sm + C::K0 + rr * (2 * D) + ((c & ~7) << 4) + (((c ^ rr) & 7) << 4)) = w;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -183,79 +246,57 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
     regs_down<C::R_CV>();
     const bool keys = warp < C::SM_WARPS + 4;
     const int w4 = (warp - C::SM_WARPS) & 3;
+    // the query rows must have been read before operands take their place
+    bool ok = true;
+    for (int t = 0; t < MT; ++t) ok = ok && mbar_wait_bounded(q_full + 8 * t, 0, a.wait_limit);
+    ok = __all_sync(FULL, ok);
+    if (!ok && lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
+    auto entry = [&](int i, int q) {  // table entry of block q of tile i
+      return aw_block_entry(a, b, aw_block(bl, min(4 * (tile0 + i) + q, bl.n - 1)));
+    };
     if (keys) {
-      // ---- key codes -> K tiles: row 16 w4 + lane % 16, half (lane / 16) of its dims
+      // ---- key codes -> K operands: row 16 w4 + lane % 16, half (lane / 16) of its dims
       constexpr int HB = PK / 2, HW = HB / 4;
       const int row = 16 * w4 + (lane & 15), half = lane >> 4;
-      const uint32_t lut = base + C::T0 + (lane & 15) * 4u;
+      [[maybe_unused]] const uint32_t lut = base + C::T0 + (lane & 15) * 4u;
+      [[maybe_unused]] const uint32_t k_lo = a.k_lev[0] | (uint32_t)a.k_lev[1] << 16,
+                                      k_hi = a.k_lev[2] | (uint32_t)a.k_lev[3] << 16;
       uint32_t cw[HW];
-      float nk[2], nv[2];  // of positions lane, lane + 32 (first warp)
+      int next = 0;  // table entry of the tile after the loaded one
       auto fetch = [&](int i) {
-        const int m = 4 * (tile0 + i) + w4;
-        const int j = aw_block(bl, min(m, bl.n - 1));
-        const int64_t c_row = (aw_block_row(a, b, j) + min(row & 15, sq.ctx - 1 - j * ATT_BLOCK)) * a.hkv + hk;
+        const int j = aw_block(bl, min(4 * (tile0 + i) + w4, bl.n - 1));
+        const int64_t c_row = (aw_entry_row(a, b, next) + min(row & 15, sq.ctx - 1 - j * ATT_BLOCK)) * a.hkv + hk;
         aw_load<HB, HW>(cw, a.k_packed + c_row * PK, half * HB, PK);
-        if (w4 == 0) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int mm = 4 * (tile0 + i) + 2 * h + (lane >> 4);
-            const int jj = aw_block(bl, min(mm, bl.n - 1));
-            const int64_t n_row =
-                (aw_block_row(a, b, jj) + min(lane & 15, sq.ctx - 1 - jj * ATT_BLOCK)) * a.hkv + hk;
-            nk[h] = __ldg(a.k_norms + n_row);
-            nv[h] = __ldg(a.v_norms + n_row);
-          }
-        }
+        if (i + 1 < cnt) next = entry(i + 1, w4);
       };
-      if (cnt > 0) fetch(0);
-      float v_most = 0.f, v_up = 1.f, v_inv = 1.f;
-      for (int i = 0; i < cnt; ++i) {
+      if (cnt > 0) {
+        next = entry(0, w4);
+        fetch(0);
+      }
+      for (int i = 0; i < cnt && ok; ++i) {
         const int buf = i % NBUF;
-        if (i >= NBUF && !__all_sync(FULL, mbar_wait_bounded(k_empty + 8 * buf, ((i / NBUF) - 1) & 1, a.wait_limit))) {
+        if (i >= NBUF) ok = __all_sync(FULL, mbar_wait_bounded(k_empty + 8 * buf, ((i / NBUF) - 1) & 1, a.wait_limit));
+        if (!ok) {
           if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
           break;
-        }
-        if (w4 == 0) {
-          TwSlot& s = reinterpret_cast<TwSlot*>(sm + C::N0)[i % TW_SLOTS];
-          float most = 0.f;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int mm = 4 * (tile0 + i) + 2 * h + (lane >> 4);
-            const float v = fabsf(nv[h]);
-            if (mm < bl.n && aw_block(bl, mm) * ATT_BLOCK + (lane & 15) <= p_hi && v < INFINITY) most = fmaxf(most, v);
-          }
-#pragma unroll
-          for (int m = 16; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL, most, m));
-          float fix = 1.f;
-          if (most > v_most) {
-            v_most = most;
-            float inv;
-            const float up = aw_pow2_for<5>(most, inv);  // weights reach 2^8: 2^14 in fp16
-            fix = up * v_inv;
-            v_up = up;
-            v_inv = inv;
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            s.nk[32 * h + lane] = nk[h];
-            s.nv[32 * h + lane] = nv[h] * v_up;
-          }
-          if (lane < 4) {
-            const int mm = 4 * (tile0 + i) + lane;
-            s.blk_t[lane] = mm < bl.n ? aw_block(bl, mm) * ATT_BLOCK : INT_MAX - 64;
-          }
-          if (lane == 0) {
-            s.v_fix = fix;
-            s.v_inv = v_inv;
-          }
-          mbar_arrive(n_full + 8 * (i % TW_SLOTS));
         }
         uint8_t* dst = sm + C::K0 + buf * C::KV + row * 128;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {  // 8 dims each
           uint32_t w[4];
+          if constexpr (KB == 2) {
+            const uint32_t codes = cw[c / 2] >> (16 * (c & 1));
+            uint32_t p[4];  // levels of codes q, q + 4
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = lds32(aw_bits<2 * KB>(cw, (4 * c + k) * 2 * KB) * 64u + lut);
+            for (int q = 0; q < 4; ++q) p[q] = tw_levels2(codes >> (2 * q), k_lo, k_hi);
+            w[0] = __byte_perm(p[0], p[1], 0x5410);
+            w[1] = __byte_perm(p[2], p[3], 0x5410);
+            w[2] = __byte_perm(p[0], p[1], 0x7632);
+            w[3] = __byte_perm(p[2], p[3], 0x7632);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = lds32(aw_bits<2 * KB>(cw, (4 * c + k) * 2 * KB) * 64u + lut);
+          }
           const int chunk = half * (D / 16) + c;  // 16-byte chunk of the row: atom chunk / 8
           *reinterpret_cast<uint4*>(dst + (chunk >> 3) * (TW_TP * 128) + (((chunk & 7) ^ (row & 7)) << 4)) =
               make_uint4(w[0], w[1], w[2], w[3]);
@@ -265,19 +306,21 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
         mbar_arrive(k_full + 8 * buf);
       }
     } else {
-      // ---- value codes -> V tiles: positions 8 pg ..., dims 8 dg ... of a thread
+      // ---- value codes -> V operands: positions 8 pg ..., dims 8 dg ... of a thread
       constexpr int DG = D / 8, PASS = D == 256 ? 2 : 1;  // 128 threads cover 128 / DG groups of 8 positions
       const int t = w4 * 32 + lane, dg = t % DG, pg0 = t / DG;
       const bool on = D > 64 || pg0 < 8;
-      const uint32_t lut = base + C::T0 + C::K_TAB * (KB == VB ? 0 : 1) + (lane & 15) * 4u;
+      [[maybe_unused]] const uint32_t lut = base + C::T0 + C::K_TAB * (KB == VB ? 0 : 1) + (lane & 15) * 4u;
+      [[maybe_unused]] const uint32_t v_lo = a.v_lev[0] | (uint32_t)a.v_lev[1] << 16,
+                                      v_hi = a.v_lev[2] | (uint32_t)a.v_lev[3] << 16;
       uint32_t vw[PASS][8];
+      int next[PASS];
       auto fetch = [&](int i) {
 #pragma unroll
         for (int q = 0; q < PASS; ++q) {
           const int pg = pg0 + q * (128 / DG);
-          const int m = 4 * (tile0 + i) + (pg >> 1);
-          const int j = aw_block(bl, min(m, bl.n - 1));
-          const int64_t row0 = aw_block_row(a, b, j);
+          const int j = aw_block(bl, min(4 * (tile0 + i) + (pg >> 1), bl.n - 1));
+          const int64_t row0 = aw_entry_row(a, b, next[q]);
           const int most = sq.ctx - 1 - j * ATT_BLOCK;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -286,12 +329,18 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
             aw_load<VB, 1>(w, a.v_packed + v_row * PV, dg * VB, PV);
             vw[q][k] = w[0];
           }
+          if (i + 1 < cnt) next[q] = entry(i + 1, pg >> 1);
         }
       };
-      if (cnt > 0 && on) fetch(0);
-      for (int i = 0; i < cnt; ++i) {
+      if (cnt > 0 && on) {
+#pragma unroll
+        for (int q = 0; q < PASS; ++q) next[q] = entry(0, (pg0 + q * (128 / DG)) >> 1);
+        fetch(0);
+      }
+      for (int i = 0; i < cnt && ok; ++i) {
         const int buf = i % NBUF;
-        if (i >= NBUF && !__all_sync(FULL, mbar_wait_bounded(v_empty + 8 * buf, ((i / NBUF) - 1) & 1, a.wait_limit))) {
+        if (i >= NBUF) ok = __all_sync(FULL, mbar_wait_bounded(v_empty + 8 * buf, ((i / NBUF) - 1) & 1, a.wait_limit));
+        if (!ok) {
           if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
           break;
         }
@@ -300,19 +349,32 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
           for (int q = 0; q < PASS; ++q) {
             const int pg = pg0 + q * (128 / DG);
             uint8_t* dst = sm + C::V0 + buf * C::KV + dg * 128 + ((pg ^ (dg & 7)) << 4);
+            if constexpr (VB == 2) {
+              uint32_t pair[4];  // code bytes of two positions, interleaved: dims 0-3, then 4-7
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {  // dims 8 dg + 2 j, + 1
-              uint32_t l[8];
+              for (int k = 0; k < 4; ++k) pair[k] = __byte_perm(vw[q][2 * k], vw[q][2 * k + 1], 0x5140);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) l[k] = lds32(((vw[q][k] >> (2 * VB * j)) & ((1u << 2 * VB) - 1u)) * 64u + lut);
-              uint32_t e[4], o[4];
+              for (int j = 0; j < 8; ++j) {
+                uint32_t e[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                e[k] = __byte_perm(l[2 * k], l[2 * k + 1], 0x5410);
-                o[k] = __byte_perm(l[2 * k], l[2 * k + 1], 0x7632);
+                for (int k = 0; k < 4; ++k) e[k] = tw_levels2(pair[k] >> (16 * (j >> 2) + 2 * (j & 3)), v_lo, v_hi);
+                *reinterpret_cast<uint4*>(dst + j * DG * 128) = make_uint4(e[0], e[1], e[2], e[3]);
               }
-              *reinterpret_cast<uint4*>(dst + (2 * j) * DG * 128) = make_uint4(e[0], e[1], e[2], e[3]);
-              *reinterpret_cast<uint4*>(dst + (2 * j + 1) * DG * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {  // dims 8 dg + 2 j, + 1
+                uint32_t l[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) l[k] = lds32(((vw[q][k] >> (2 * VB * j)) & ((1u << 2 * VB) - 1u)) * 64u + lut);
+                uint32_t e[4], o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  e[k] = __byte_perm(l[2 * k], l[2 * k + 1], 0x5410);
+                  o[k] = __byte_perm(l[2 * k], l[2 * k + 1], 0x7632);
+                }
+                *reinterpret_cast<uint4*>(dst + (2 * j) * DG * 128) = make_uint4(e[0], e[1], e[2], e[3]);
+                *reinterpret_cast<uint4*>(dst + (2 * j + 1) * DG * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+              }
             }
           }
           if (i + 1 < cnt) fetch(i + 1);
@@ -349,25 +411,103 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
           umma_commit(k_empty + 8 * buf);
         }
         if (i > 0) {
-          const int j = i - 1, buf = j % NBUF;
-          ok = mbar_wait_bounded(v_full + 8 * buf, (j / NBUF) & 1, a.wait_limit) &&
-               mbar_wait_bounded(p_full + 16 * t + 8 * (j & 1), (j >> 1) & 1, a.wait_limit);
+          const int u = i - 1, buf = u % NBUF;
+          ok = mbar_wait_bounded(v_full + 8 * buf, (u / NBUF) & 1, a.wait_limit) &&
+               mbar_wait_bounded(p_full + 16 * t + 8 * (u & 1), (u >> 1) & 1, a.wait_limit);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t p = s0 + 64u * (j & 1);
+          const uint32_t p = s0 + 64u * (u & 1);
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int ks = 0; ks < TW_TP / 16; ++ks)
               umma_f16_ts(o0, p + (uint32_t)(32 * part + 8 * ks), v_desc + ((buf * C::KV + ks * 32) >> 4), ID_O,
-                          part + ks > 0 || j > 0);
-          umma_commit(o_done + 16 * t + 8 * (j & 1));
+                          part + ks > 0 || u > 0);
+          umma_commit(o_done + 16 * t + 8 * (u & 1));
           umma_commit(v_empty + 8 * buf);
         }
       }
       if (!ok) record_error(a.err, TQ_DEVERR_TIMEOUT);
       umma_commit(mma_end + 8 * t);
       if (!mbar_wait_bounded(mma_end + 8 * t, 0, a.wait_limit)) record_error(a.err, TQ_DEVERR_TIMEOUT);
+    } else if (t == 2) {
+      // ---- norms and positions of the tiles, two positions per lane. A slot is
+      // free again when the product two tiles back has read its keys (its
+      // issuer had the weights of the tile four back).
+      const int q = lane >> 4;
+      float nk[2], nv[2];
+      int next[2];
+      auto entry = [&](int i, int h) {
+        return aw_block_entry(a, b, aw_block(bl, min(4 * (tile0 + i) + 2 * h + q, bl.n - 1)));
+      };
+      auto fetch = [&](int i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int j = aw_block(bl, min(4 * (tile0 + i) + 2 * h + q, bl.n - 1));
+          const int64_t n_row =
+              (aw_entry_row(a, b, next[h]) + min(lane & 15, sq.ctx - 1 - j * ATT_BLOCK)) * a.hkv + hk;
+          nk[h] = __ldg(a.k_norms + n_row);
+          nv[h] = __ldg(a.v_norms + n_row);
+          if (i + 1 < cnt) next[h] = entry(i + 1, h);
+        }
+      };
+      if (cnt > 0) {
+        next[0] = entry(0, 0);
+        next[1] = entry(0, 1);
+        fetch(0);
+      }
+      float v_most = 0.f, v_up = 1.f, v_inv = 1.f;
+      for (int i = 0; i < cnt; ++i) {
+        const int buf = i % NBUF;
+        if (i >= NBUF && !__all_sync(FULL, mbar_wait_bounded(k_empty + 8 * buf, ((i / NBUF) - 1) & 1, a.wait_limit))) {
+          if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
+          break;
+        }
+        TwSlot& s = reinterpret_cast<TwSlot*>(sm + C::N0)[i % TW_SLOTS];
+        float most = 0.f;
+        int t_min = INT_MAX, t_max = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int m = 4 * (tile0 + i) + 2 * h + q;
+          const int at = m < bl.n ? aw_block(bl, m) * ATT_BLOCK : INT_MAX - 64;
+          const float v = fabsf(nv[h]);
+          if (at + (lane & 15) <= p_hi && v < INFINITY) most = fmaxf(most, v);
+          t_min = min(t_min, at);
+          t_max = max(t_max, at + ATT_BLOCK - 1);
+          if ((lane & 15) == 0) s.blk_t[2 * h + q] = at;
+        }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL, most, m));
+        t_min = min(t_min, __shfl_xor_sync(FULL, t_min, 16));
+        t_max = max(t_max, __shfl_xor_sync(FULL, t_max, 16));
+        float fix = 1.f;
+        if (most > v_most) {
+          v_most = most;
+          float inv;
+          const float up = aw_pow2_for<5>(most, inv);  // weights reach 2^8: 2^14 in fp16
+          fix = up * v_inv;
+          v_up = up;
+          v_inv = inv;
+        }
+        bool fine = true;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          s.nk[32 * h + lane] = nk[h];
+          s.nv[32 * h + lane] = nv[h] * v_up;
+          fine = fine && fabsf(nk[h]) < INFINITY && fabsf(nv[h]) < INFINITY;
+        }
+        fine = __all_sync(FULL, fine);
+        if (lane == 0) {
+          s.t_min = t_min;
+          s.t_max = t_max;
+          s.v_fix = fix;
+          s.v_inv = v_inv;
+          s.odd = !fine;
+        }
+        if (i + 1 < cnt) fetch(i + 1);
+        mbar_arrive(n_full + 8 * (i % TW_SLOTS));
+        mbar_arrive(k_full + 8 * buf);
+      }
     }
   } else {
     regs_up<C::R_SM>();
@@ -379,13 +519,14 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
     const int64_t out_row = (sq.q0 + q_i) * a.hq + hk * a.g + q_h;
     float row_inv = 1.f;
     if (row_ok) {
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + out_row * D);
+      const uint8_t* src = sm + C::K0 + tid * (2 * D);
+      const int sw = (tid & 7) << 4;
       float ss = 0.f;
-  #pragma unroll 4
+#pragma unroll 4
       for (int e = 0; e < D / 8; ++e) {
-        const uint4 w = __ldg(src + e);
+        const uint4 w = *reinterpret_cast<const uint4*>(src + ((e & ~7) << 4) + (((e & 7) << 4) ^ sw));
         const uint32_t hw[4] = {w.x, w.y, w.z, w.w};
-  #pragma unroll
+#pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hw[c]));
           ss = fmaf(f.x, f.x, fmaf(f.y, f.y, ss));
@@ -394,19 +535,19 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
       // no rotated coordinate exceeds sqrt(d) |q|: that bound is put just below 2^15
       const float up = aw_pow2_for<14>(sqrtf(ss * (float)D) * a.q_scale, row_inv);
       const float qs = a.q_scale * up;
-  #pragma unroll 1
+#pragma unroll 1
       for (int hf = 0; hf < D / 64; ++hf) {
         float x[64];
-  #pragma unroll
+#pragma unroll
         for (int e = 0; e < 64; ++e) x[e] = 0.f;
-  #pragma unroll 1
+#pragma unroll 1
         for (int m = 0; m < D / 64; ++m) {
           const float sg = (__popc(m & hf) & 1) ? -1.f : 1.f;
-  #pragma unroll
+#pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const uint4 w = __ldg(src + 8 * m + e);
+            const uint4 w = *reinterpret_cast<const uint4*>(src + (m << 7) + ((e << 4) ^ sw));
             const uint32_t hw[4] = {w.x, w.y, w.z, w.w};
-  #pragma unroll
+#pragma unroll
             for (int c = 0; c < 4; ++c) {
               const uint32_t s = hw[c] ^ a.k_sign_h2[32 * m + 4 * e + c];
               const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&s));
@@ -415,12 +556,12 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
             }
           }
         }
-        wht64(x);
+      wht64(x);
         uint8_t* dst = sm + C::Q0 + 2 * mt * C::Q_PART + hf * 16384 + r_tile * 128;
-  #pragma unroll
+#pragma unroll
         for (int c = 0; c < 8; ++c) {
           uint32_t hi[4], lo[4];
-  #pragma unroll
+#pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float u = x[8 * c + 2 * k] * qs, v = x[8 * c + 2 * k + 1] * qs;
             hi[k] = pack_half2(u, v);
@@ -436,7 +577,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
     if (!row_ok) {  // rows behind the last: scores of 0
       uint4* dst = reinterpret_cast<uint4*>(sm + C::Q0 + 2 * mt * C::Q_PART + r_tile * 128);
       for (int e = 0; e < 2 * (D / 64); ++e)
-  #pragma unroll
+#pragma unroll
         for (int c = 0; c < 8; ++c) dst[e * (16384 / 16) + c] = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
@@ -480,25 +621,29 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
           const f2 v = mul2(make_float2(x[c + 2], x[c + 3]), make_float2(n.z, n.w));
           x[c] = u.x, x[c + 1] = u.y, x[c + 2] = v.x, x[c + 3] = v.y;
         }
-        uint32_t hidden = 0;  // blocks with masked positions for this warp's rows
+        // whether some position is masked for some row of the warp
+        const bool hidden =
+            !(slot.t_max <= pw_lo && (slot.t_max < a.sinks || slot.t_min > pw_hi - a.window));
+        if (hidden) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int t0 = slot.blk_t[h], t1 = t0 + ATT_BLOCK - 1;
-          if (t1 <= pw_lo && (t1 < a.sinks || t0 > pw_hi - a.window)) continue;
-          hidden |= 1u << h;
+          for (int h = 0; h < 4; ++h) {
+            const int t0 = slot.blk_t[h];
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            if (!aw_visible(t0 + c, p_row, a.window, a.sinks)) x[16 * h + c] = -INFINITY;
+            for (int c = 0; c < 16; ++c)
+              if (!aw_visible(t0 + c, p_row, a.window, a.sinks)) x[16 * h + c] = -INFINITY;
+          }
         }
         float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
 #pragma unroll
-        for (int c = 4; c < 64; c += 4) {
-          mx0 = fmaxf(mx0, x[c]);
-          mx1 = fmaxf(mx1, x[c + 1]);
-          mx2 = fmaxf(mx2, x[c + 2]);
-          mx3 = fmaxf(mx3, x[c + 3]);
+        for (int c = 4; c < 60; c += 8) {
+          mx0 = tw_max3(mx0, x[c], x[c + 1]);
+          mx1 = tw_max3(mx1, x[c + 2], x[c + 3]);
+          mx2 = tw_max3(mx2, x[c + 4], x[c + 5]);
+          mx3 = tw_max3(mx3, x[c + 6], x[c + 7]);
         }
-        const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * row_inv;
+        mx0 = tw_max3(mx0, x[60], x[61]);
+        mx1 = tw_max3(mx1, x[62], x[63]);
+        const float mx = fmaxf(tw_max3(mx0, mx1, mx2), mx3) * row_inv;
         // the reference follows the maximum when it is exceeded by 2^8
         const bool move = mx > m_ref + 8.0f || (m_ref == -INFINITY && mx != -INFINITY);
         const float v_fix = slot.v_fix;
@@ -535,36 +680,10 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
           }
         }
         const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-        float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-        for (int c0 = 0; c0 < 64; c0 += 32) {
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const float4 n = *reinterpret_cast<const float4*>(slot.nv + c0 + c);
-            const float nn[4] = {n.x, n.y, n.z, n.w};
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int e = c0 + c + 2 * k;
-              const f2 z = fma2(make_float2(x[e], x[e + 1]), make_float2(row_inv, row_inv), make_float2(-ref, -ref));
-              const f2 p = make_float2(aw_exp2(z.x), aw_exp2(z.y));
-              sum0 += p.x;
-              sum1 += p.y;
-              f2 w = mul2(p, make_float2(nn[2 * k], nn[2 * k + 1]));
-              if (hidden >> (e / 16) & 1u) {  // a masked norm may be anything
-                if (x[e] == -INFINITY) w.x = 0.f;
-                if (x[e + 1] == -INFINITY) w.y = 0.f;
-              }
-              const uint32_t h2 = pack_half2(w.x, w.y);
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-              hi[c / 2 + k] = h2;
-              lo[c / 2 + k] = pack_half2(w.x - f.x, w.y - f.y);
-            }
-          }
-          tmem_st16(sp + (uint32_t)(c0 / 2), hi);
-          tmem_st16(sp + 32u + (uint32_t)(c0 / 2), lo);
-        }
-        l_sum += sum0 + sum1;
+        // a masked position's norm may be infinite or NaN: its weight is then
+        // cleared by comparison instead of by its factor 0
+        l_sum += hidden && slot.odd ? tw_weights<true>(x, slot.nv, row_inv, ref, sp)
+                                    : tw_weights<false>(x, slot.nv, row_inv, ref, sp);
         tmem_wait_st();
       }
       tc_fence_before();
@@ -577,13 +696,17 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
       tc_fence_after();
     }
     if (any_row && ok) {
-      const bool empty = cnt == 0 || m_ref == -INFINITY;
       const int64_t idx = out_row * a.n_split + split;
       if (a.n_split > 1 && row_ok) {
-        a.ws_m[idx] = empty && l_sum == 0.f ? -INFINITY : m_ref;
+        a.ws_m[idx] = m_ref;
         a.ws_l[idx] = l_sum;
       }
+      // NaN where the sum is NaN, 0 where no position was seen
       const float scale = a.n_split > 1 ? v_inv : (l_sum > 0.f ? v_inv * a.o_scale / l_sum : (l_sum == l_sum ? 0.f : l_sum));
+      // rows of the warp are put together in the row tile's query operand
+      // (no product reads it any more; 4 d bytes per row, 16-byte chunks
+      // swizzled within 128 bytes) and leave in whole lines
+      uint8_t* stage = sm + C::Q0 + 2 * mt * C::Q_PART + 32 * (warp & 3) * (4 * D);
 #pragma unroll 1
       for (int hf = 0; hf < D / 64; ++hf) {
         float x[64];
@@ -608,24 +731,27 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
         // column 64 hf + e is dim 8 (e % DG) + JN hf + e / DG: JN neighbouring dims per group
         constexpr int DG = D / 8, JN = 64 / DG;
 #pragma unroll
-        for (int dg = 0; dg < DG && row_ok; ++dg) {
-          float y[JN];
-#pragma unroll
-          for (int j = 0; j < JN; ++j) y[j] = x[j * DG + dg] * scale;
+        for (int dg = 0; dg < DG; ++dg) {
           const int dim = 8 * dg + JN * hf;
-          if (a.n_split > 1) {
-            if (!empty) {
-              float2* dst = reinterpret_cast<float2*>(a.ws_acc + idx * D + dim);
 #pragma unroll
-              for (int j = 0; j < JN; j += 2) dst[j / 2] = make_float2(y[j], y[j + 1]);
-            }
-          } else {
-            uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + out_row * D + dim);
-#pragma unroll
-            for (int j = 0; j < JN; j += 2)
-              dst[j / 2] = empty && l_sum == 0.f ? 0u : pack_half2(y[j], y[j + 1]) ^ a.v_sign_h2[(dim + j) / 2];
+          for (int j = 0; j < JN; j += 2) {
+            const float u = x[j * DG + dg] * scale, v = x[(j + 1) * DG + dg] * scale;
+            const int at = (a.n_split > 1 ? 4 : 2) * (dim + j);
+            uint8_t* dst = stage + lane * (4 * D) + (at & ~112) + ((at ^ (lane << 4)) & 112);
+            if (a.n_split > 1) *reinterpret_cast<float2*>(dst) = make_float2(u, v);
+            else *reinterpret_cast<uint32_t*>(dst) = pack_half2(u, v) ^ a.v_sign_h2[(dim + j) / 2];
           }
         }
+      }
+      __syncwarp();
+      const int chunks = a.n_split > 1 ? D / 4 : D / 8;  // of 16 bytes, per row
+      uint8_t* to = a.n_split > 1 ? reinterpret_cast<uint8_t*>(a.ws_acc) : reinterpret_cast<uint8_t*>(a.out);
+      const int64_t row_to = a.n_split > 1 ? idx : out_row;
+      for (int e = lane; e < 32 * chunks; e += 32) {
+        const int rr = e / chunks, c = e % chunks;
+        const int64_t at = __shfl_sync(FULL, row_to, rr) * (16 * chunks) + 16 * c;
+        const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * (4 * D) + ((c & ~7) << 4) + (((c ^ rr) & 7) << 4));
+        if (rw0 + rr < rows) *reinterpret_cast<uint4*>(to + at) = w;
       }
     }
   }

@@ -190,6 +190,21 @@ def test_non_finite_norms_where_no_query_looks(K):
     assert torch.equal(ref[1], got[1]) and torch.equal(ref[0, :4], got[0, :4]) and got[0, 4:].isnan().all()
 
 
+@pytest.mark.parametrize("n,S", [(1, 40), (1, 2000), (40, 100), (40, 3000)])
+def test_a_nan_query_gives_its_own_rows_nan(K, n, S):
+    """One and several splits, few and many query rows."""
+    d, hq, hkv = 128, 4, 2
+    kc, kp, kn = _cache(K, (1, S, hkv), d, 4, 1)
+    vc, vp, vn = _cache(K, (1, S, hkv), d, 2, 2)
+    q = torch.randn(n, hq, d, device="cuda").half()
+    q[n // 2, 1, 7] = float("nan")
+    o = K.attend_window(q, kc, vc, kp, kn, vp, vn, torch.tensor([S], dtype=torch.int32, device="cuda"),
+                        q_offsets=torch.tensor([0, n], dtype=torch.int32, device="cuda"), max_q=n)
+    nan = torch.zeros(n, hq, dtype=torch.bool, device="cuda")
+    nan[n // 2, 1] = True
+    assert torch.equal(o.isnan().all(-1), nan) and torch.equal(o.isnan().any(-1), nan)
+
+
 @pytest.mark.parametrize("k_norm,v_norm,q_size", [(1e6, 1e6, 1e-4), (1e-6, 1e-6, 100.0), (1e-30, 1e4, 1.0), (30.0, 1e-20, 1e-3)])
 def test_norms_and_queries_of_any_size(K, k_norm, v_norm, q_size):
     """Norms far outside fp16 (stored as f32) neither overflow nor vanish:
