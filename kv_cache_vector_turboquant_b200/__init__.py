@@ -134,15 +134,19 @@ def _one_device(names, tensors) -> int:
     return dev
 
 
-def _run(dev: int, stream, call, *args):
-    """call(raw stream, *args) with device `dev` current, on `stream` or that
-    device's current stream; what `call` allocates belongs to the stream."""
+def _elsewhere(dev: int, stream) -> bool:
+    """Whether a call has to be made inside `_launching`: a stream is given, or
+    the tensors' device is not the current one."""
     import torch
 
-    if stream is None and torch.cuda.current_device() == dev:
-        return call(torch._C._cuda_getCurrentRawStream(dev), *args)
-    with _launching(torch.device("cuda", dev), stream):
-        return call(torch.cuda.current_stream().cuda_stream, *args)
+    return stream is not None or torch.cuda.current_device() != dev
+
+
+def _raw_stream(dev: int) -> int:
+    """Handle of the current stream of the current device."""
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 class TurboQuant:
@@ -483,10 +487,10 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
 
 
 def _head_rows(t, name):
-    """Checks of a [T, H, d] view whose rows are dense and 16-byte aligned."""
+    """Strides of a [T, H, d] view whose rows are dense and 16-byte aligned."""
     s0, s1, s2 = t.stride()
-    _require(s2 == 1 and s0 % 8 == 0 and s1 % 8 == 0 and t.data_ptr() % 16 == 0,
-             f"{name}: dense rows, 16-byte aligned, strides multiples of 8 elements")
+    if s2 != 1 or (s0 | s1) & 7 or t.data_ptr() & 15:
+        raise ValueError(f"{name}: dense rows, 16-byte aligned, strides multiples of 8 elements")
     return s0, s1
 
 
@@ -506,47 +510,56 @@ def qk_norm_rope(q, k, positions, inv_freq=None, *, interleaved: bool = False, r
     import torch
 
     half = torch.float16
-    _require(isinstance(q, torch.Tensor) and isinstance(k, torch.Tensor) and q.dim() == 3 and k.dim() == 3,
-             "q: [T, Hq, d]; k: [T, Hkv, d]")
+    if not (isinstance(q, torch.Tensor) and isinstance(k, torch.Tensor) and q.dim() == 3 and k.dim() == 3):
+        raise ValueError("q: [T, Hq, d]; k: [T, Hkv, d]")
     T, hq, d = q.shape
-    hkv = k.shape[1]
-    _require(k.shape[0] == T and k.shape[2] == d, "q: [T, Hq, d]; k: [T, Hkv, d] with the same T and d")
-    _require(d in (64, 128, 256), f"head_dim: 64, 128 or 256, got {d}")
-    _require(hq > 0 and hkv > 0, "q, k: at least one head")
-    _require(q.dtype in (half, torch.bfloat16) and k.dtype == q.dtype,
-             f"q, k: both float16 or both bfloat16, got {q.dtype} and {k.dtype}")
-    qs, ks = _head_rows(q, "q"), _head_rows(k, "k")
+    Tk, hkv, dk = k.shape
+    if Tk != T or dk != d:
+        raise ValueError("q: [T, Hq, d]; k: [T, Hkv, d] with the same T and d")
+    if d not in (64, 128, 256):
+        raise ValueError(f"head_dim: 64, 128 or 256, got {d}")
+    if not (hq and hkv):
+        raise ValueError("q, k: at least one head")
+    kind = q.dtype
+    if (kind is not half and kind is not torch.bfloat16) or k.dtype is not kind:
+        raise ValueError(f"q, k: both float16 or both bfloat16, got {q.dtype} and {k.dtype}")
+    q0, q1 = _head_rows(q, "q")
+    k0, k1 = _head_rows(k, "k")
     _check(positions, "positions", torch.int32, numel=T)
     rot = 0
     if inv_freq is not None:
         _check(inv_freq, "inv_freq", torch.float64)
         rot = 2 * inv_freq.numel()
-        _require(rot <= d, f"inv_freq: at most {d // 2} frequencies, got {rot // 2}")
+        if rot > d:
+            raise ValueError(f"inv_freq: at most {d // 2} frequencies, got {rot // 2}")
     w_type = None
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None:
-            _check(w, name, torch.float32 if w.dtype is torch.float32 else (q.dtype, torch.float32), numel=d)
-            _require(w.data_ptr() % 16 == 0, f"{name}: 16-byte aligned")
-            _require(w_type is None or w_type is w.dtype, "q_weight, k_weight: the same dtype")
+            _check(w, name, kind if w.dtype is kind else (kind, torch.float32), numel=d)
+            if w.data_ptr() & 15:
+                raise ValueError(f"{name}: 16-byte aligned")
+            if w_type is not None and w_type is not w.dtype:
+                raise ValueError("q_weight, k_weight: the same dtype")
             w_type = w.dtype
-    _require(eps >= 0.0, "eps: >= 0")
+    if not eps >= 0.0:
+        raise ValueError("eps: >= 0")
     qo, ko = out if out is not None else (None, None)
     if out is not None:
         _check(qo, "out q", half, shape=(T, hq, d))
         _check(ko, "out k", half, shape=(T, hkv, d))
     dev = _one_device(("q", "k", "positions", "inv_freq", "q_weight", "k_weight", "out q", "out k"),
                       (q, k, positions, inv_freq, q_weight, k_weight, qo, ko))
-
-    def call(raw, qo, ko):
-        if qo is None:
-            qo = torch.empty((T, hq, d), dtype=half, device=q.device)
-            ko = torch.empty((T, hkv, d), dtype=half, device=q.device)
-        tq_qk_norm_rope(q, k, TQ_F16 if q.dtype is half else TQ_BF16, T, hq, hkv, d, qs[0], qs[1], ks[0], ks[1],
-                        positions, inv_freq, rot, interleaved, rope_scale, q_weight, k_weight,
-                        w_type is torch.float32, eps, qo, ko, raw)
-        return qo, ko
-
-    return _run(dev, stream, call, qo, ko)
+    if _elsewhere(dev, stream):
+        with _launching(q.device, stream):
+            return qk_norm_rope(q, k, positions, inv_freq, interleaved=interleaved, rope_scale=rope_scale,
+                                q_weight=q_weight, k_weight=k_weight, eps=eps, out=out)
+    if out is None:
+        qo = torch.empty((T, hq, d), dtype=half, device=q.device)
+        ko = torch.empty((T, hkv, d), dtype=half, device=q.device)
+    tq_qk_norm_rope(q, k, TQ_F16 if kind is half else TQ_BF16, T, hq, hkv, d, q0, q1, k0, k1, positions, inv_freq,
+                    rot, interleaved, rope_scale, q_weight, k_weight, w_type is torch.float32, eps, qo, ko,
+                    _raw_stream(dev))
+    return qo, ko
 
 
 def _window_args(q, k_codec, v_codec, q_offsets, max_q, n_seq, hkv, window, sinks, out, workspace):
@@ -554,16 +567,22 @@ def _window_args(q, k_codec, v_codec, q_offsets, max_q, n_seq, hkv, window, sink
 
     T, hq, d = q.shape
     _check(q, "q", torch.float16, shape=(T, hq, k_codec.head_dim))
-    _require(k_codec.head_dim == v_codec.head_dim, "k_codec, v_codec: the same head_dim")
-    _require(hkv > 0 and hq > 0 and hq % hkv == 0, f"q: a multiple of {hkv} heads, got {hq}")
-    _require(window is None or int(window) >= 1, "window: None or at least 1")
-    _require(int(sinks) >= 0, "sinks: at least 0")
+    if d != v_codec.head_dim:
+        raise ValueError("k_codec, v_codec: the same head_dim")
+    if not (hkv > 0 and hq > 0 and hq % hkv == 0):
+        raise ValueError(f"q: a multiple of {hkv} heads, got {hq}")
+    if window is not None and int(window) < 1:
+        raise ValueError("window: None or at least 1")
+    if int(sinks) < 0:
+        raise ValueError("sinks: at least 0")
     if q_offsets is None:
-        _require(T == n_seq and max_q in (None, 1), "q: one token per sequence where q_offsets is None")
+        if T != n_seq or max_q not in (None, 1):
+            raise ValueError("q: one token per sequence where q_offsets is None")
         max_q = 1
     else:
         _check(q_offsets, "q_offsets", torch.int32, numel=n_seq + 1)
-        _require(max_q is not None and int(max_q) >= 1, "max_q: the largest number of tokens of a sequence")
+        if max_q is None or int(max_q) < 1:
+            raise ValueError("max_q: the largest number of tokens of a sequence")
     if out is not None:
         _check(out, "out", torch.float16, shape=(T, hq, d))
     if workspace is not None:
@@ -586,8 +605,10 @@ def attend_window(q, k_codec: TurboQuant, v_codec: TurboQuant, k_packed, k_norms
     """
     import torch
 
-    _require(q.dim() == 3 and k_packed.dim() == 4, "q: [T, Hq, d]; k_packed: [B, S, Hkv, Pk]")
-    B, s_max, hkv = k_packed.shape[0], k_packed.shape[1], k_packed.shape[2]
+    if q.dim() != 3 or k_packed.dim() != 4:
+        raise ValueError("q: [T, Hq, d]; k_packed: [B, S, Hkv, Pk]")
+    B, s_max, hkv, _ = k_packed.shape
+    given = window  # as the caller has it, for a call made again inside another device or stream
     T, hq, d, max_q, window, sinks = _window_args(q, k_codec, v_codec, q_offsets, max_q, B, hkv, window, sinks, out,
                                                   workspace)
     _check(k_packed, "k_packed", torch.uint8, shape=(B, s_max, hkv, k_codec.packed_bytes))
@@ -598,19 +619,19 @@ def attend_window(q, k_codec: TurboQuant, v_codec: TurboQuant, k_packed, k_norms
     dev = _one_device(("q", "q_offsets", "out", "workspace", "k_packed", "v_packed", "k_norms", "v_norms",
                        "context_lens"),
                       (q, q_offsets, out, workspace, k_packed, v_packed, k_norms, v_norms, context_lens))
-    need = tq_attend_window_workspace_bytes(T, B, max_q, hq, hkv, d, s_max, window, sinks)
-
-    def call(raw, out, workspace):
-        if out is None:
-            out = torch.empty_like(q)
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        tq_attend_window(k_codec.ctx, v_codec.ctx, q, T, B, q_offsets, max_q, hq, hkv, k_packed, k_norms, v_packed,
-                         v_norms, s_max, context_lens, window, sinks, out, workspace,
-                         0 if workspace is None else workspace.numel(), raw)
-        return out
-
-    return _run(dev, stream, call, out, workspace)
+    if _elsewhere(dev, stream):
+        with _launching(q.device, stream):
+            return attend_window(q, k_codec, v_codec, k_packed, k_norms, v_packed, v_norms, context_lens, given, sinks,
+                                 q_offsets, max_q, out, workspace)
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        need = tq_attend_window_workspace_bytes(T, B, max_q, hq, hkv, d, s_max, window, sinks)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    tq_attend_window(k_codec.ctx, v_codec.ctx, q, T, B, q_offsets, max_q, hq, hkv, k_packed, k_norms, v_packed,
+                     v_norms, s_max, context_lens, window, sinks, out, workspace,
+                     0 if workspace is None else workspace.numel(), _raw_stream(dev))
+    return out
 
 
 def attend_window_paged(q, k_codec: TurboQuant, v_codec: TurboQuant, k_cache, k_norms, v_cache, v_norms,
@@ -622,11 +643,13 @@ def attend_window_paged(q, k_codec: TurboQuant, v_codec: TurboQuant, k_cache, k_
     (`pages_trim`)."""
     import torch
 
-    _require(q.dim() == 3 and k_cache.dim() == 4 and block_tables.dim() == 2,
-             "q: [T, Hq, d]; k_cache: [num_blocks, 16, Hkv, Pk]; block_tables: [B, max_blocks]")
-    num_blocks, blk, hkv = k_cache.shape[0], k_cache.shape[1], k_cache.shape[2]
-    _require(blk == TQ_PAGE_BLOCK, f"cache blocks must hold {TQ_PAGE_BLOCK} positions")
+    if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2:
+        raise ValueError("q: [T, Hq, d]; k_cache: [num_blocks, 16, Hkv, Pk]; block_tables: [B, max_blocks]")
+    num_blocks, blk, hkv, _ = k_cache.shape
+    if blk != TQ_PAGE_BLOCK:
+        raise ValueError(f"cache blocks must hold {TQ_PAGE_BLOCK} positions")
     B, max_blocks = block_tables.shape
+    given = window  # as the caller has it, for a call made again inside another device or stream
     T, hq, d, max_q, window, sinks = _window_args(q, k_codec, v_codec, q_offsets, max_q, B, hkv, window, sinks, out,
                                                   workspace)
     _check(k_cache, "k_cache", torch.uint8, shape=(num_blocks, blk, hkv, k_codec.packed_bytes))
@@ -638,19 +661,19 @@ def attend_window_paged(q, k_codec: TurboQuant, v_codec: TurboQuant, k_cache, k_
     dev = _one_device(("q", "q_offsets", "out", "workspace", "k_cache", "v_cache", "k_norms", "v_norms",
                        "block_tables", "context_lens"),
                       (q, q_offsets, out, workspace, k_cache, v_cache, k_norms, v_norms, block_tables, context_lens))
-    need = tq_attend_window_workspace_bytes(T, B, max_q, hq, hkv, d, max_blocks * TQ_PAGE_BLOCK, window, sinks)
-
-    def call(raw, out, workspace):
-        if out is None:
-            out = torch.empty_like(q)
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        tq_attend_window_paged(k_codec.ctx, v_codec.ctx, q, T, B, q_offsets, max_q, hq, hkv, k_cache, k_norms,
-                               v_cache, v_norms, num_blocks, block_tables, max_blocks, context_lens, window, sinks,
-                               out, workspace, 0 if workspace is None else workspace.numel(), raw)
-        return out
-
-    return _run(dev, stream, call, out, workspace)
+    if _elsewhere(dev, stream):
+        with _launching(q.device, stream):
+            return attend_window_paged(q, k_codec, v_codec, k_cache, k_norms, v_cache, v_norms, block_tables,
+                                       context_lens, given, sinks, q_offsets, max_q, out, workspace)
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        need = tq_attend_window_workspace_bytes(T, B, max_q, hq, hkv, d, max_blocks * TQ_PAGE_BLOCK, window, sinks)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    tq_attend_window_paged(k_codec.ctx, v_codec.ctx, q, T, B, q_offsets, max_q, hq, hkv, k_cache, k_norms, v_cache,
+                           v_norms, num_blocks, block_tables, max_blocks, context_lens, window, sinks, out, workspace,
+                           0 if workspace is None else workspace.numel(), _raw_stream(dev))
+    return out
 
 
 def _page_state(block_tables, context_lens, refs, num_blocks):
@@ -658,14 +681,15 @@ def _page_state(block_tables, context_lens, refs, num_blocks):
     import torch
 
     _check(block_tables, "block_tables", torch.int32)
-    _require(block_tables.dim() == 2 and block_tables.shape[0] > 0 and block_tables.shape[1] > 0,
-             "block_tables: [rows, max_blocks]")
+    if block_tables.dim() != 2 or not block_tables.numel():
+        raise ValueError("block_tables: [rows, max_blocks]")
+    rows, max_blocks = block_tables.shape
     if context_lens is not None:
-        _check(context_lens, "context_lens", torch.int32, numel=block_tables.shape[0])
+        _check(context_lens, "context_lens", torch.int32, numel=rows)
     _check(refs, "refs", torch.int32)
-    _require(refs.dim() == 1 and refs.numel() > 0 and num_blocks in (None, refs.numel()),
-             f"refs: one count per page ({num_blocks}), got {tuple(refs.shape)}")
-    return block_tables.shape[0], block_tables.shape[1]
+    if refs.dim() != 1 or not refs.numel() or (num_blocks is not None and refs.numel() != num_blocks):
+        raise ValueError(f"refs: one count per page ({num_blocks}), got {tuple(refs.shape)}")
+    return rows, max_blocks
 
 
 def pages_trim(block_tables, context_lens, refs, window=None, sinks: int = 0, release=None, out=None, stream=None):
@@ -681,8 +705,10 @@ def pages_trim(block_tables, context_lens, refs, window=None, sinks: int = 0, re
     import torch
 
     rows, max_blocks = _page_state(block_tables, context_lens, refs, None)
-    _require(window is None or int(window) >= 0, "window: None or at least 0")
-    _require(int(sinks) >= 0, "sinks: at least 0")
+    if window is not None and int(window) < 0:
+        raise ValueError("window: None or at least 0")
+    if int(sinks) < 0:
+        raise ValueError("sinks: at least 0")
     if release is not None:
         _check(release, "release", torch.bool if release.dtype is torch.bool else (torch.bool, torch.uint8), numel=rows)
     if out is not None:
@@ -690,15 +716,14 @@ def pages_trim(block_tables, context_lens, refs, window=None, sinks: int = 0, re
         _require(out[0].shape == block_tables.shape, "out: tables of the same shape")
     dev = _one_device(("block_tables", "context_lens", "refs", "release", "out", "out", "out"),
                       (block_tables, context_lens, refs, release, *(out if out is not None else ())))
-
-    def call(raw, out):
-        t, n, r = out if out is not None else (torch.empty_like(block_tables), torch.empty_like(context_lens),
-                                               torch.empty_like(refs))
-        tq_pages_trim(block_tables, t, context_lens, n, refs, r, rows, max_blocks, refs.numel(),
-                      -1 if window is None else int(window), int(sinks), release, raw)
-        return t, n, r
-
-    return _run(dev, stream, call, out)
+    if _elsewhere(dev, stream):
+        with _launching(refs.device, stream):
+            return pages_trim(block_tables, context_lens, refs, window, sinks, release, out)
+    t, n, r = out if out is not None else (torch.empty_like(block_tables), torch.empty_like(context_lens),
+                                           torch.empty_like(refs))
+    tq_pages_trim(block_tables, t, context_lens, n, refs, r, rows, max_blocks, refs.numel(),
+                  -1 if window is None else int(window), int(sinks), release, _raw_stream(dev))
+    return t, n, r
 
 
 class TQPagePools:
@@ -731,7 +756,8 @@ class TQPagePools:
 
     def _on_mine(self, names, tensors):
         dev = _one_device(names, tensors)
-        _require(dev == self._dev, f"tensors on cuda:{self._dev} like the pools, got cuda:{dev}")
+        if dev != self._dev:
+            raise ValueError(f"tensors on cuda:{self._dev} like the pools, got cuda:{dev}")
 
     def fork(self, block_tables, context_lens, refs, parents, children, out=None, workspace=None, stream=None):
         """Make row children[i] a copy of row parents[i]: the parent's full
@@ -745,7 +771,8 @@ class TQPagePools:
         n = parents.numel()
         _check(parents, "parents", torch.int32)
         _check(children, "children", torch.int32, numel=n)
-        _require(n <= rows <= TQ_MAX_PAGE_ROWS, f"at most {rows} forks of at most {TQ_MAX_PAGE_ROWS} rows")
+        if not n <= rows <= TQ_MAX_PAGE_ROWS:
+            raise ValueError(f"at most {rows} forks of at most {TQ_MAX_PAGE_ROWS} rows")
         if out is not None:
             _page_state(*out, self.num_blocks)
             _require(out[0].shape == block_tables.shape, "out: tables of the same shape")
@@ -754,17 +781,16 @@ class TQPagePools:
         self._on_mine(("block_tables", "context_lens", "refs", "parents", "children", "workspace", "out", "out", "out"),
                       (block_tables, context_lens, refs, parents, children, workspace,
                        *(out if out is not None else ())))
-
-        def call(raw, out, workspace):
-            t, c, r = out if out is not None else (torch.empty_like(block_tables), torch.empty_like(context_lens),
-                                                   torch.empty_like(refs))
-            if workspace is None:
-                workspace = torch.empty(tq_pages_fork_workspace_bytes(n), dtype=torch.uint8, device=refs.device)
-            tq_pages_fork(self._array, len(self._array), self.num_blocks, block_tables, t, context_lens, c, refs, r,
-                          rows, max_blocks, parents, children, n, workspace, workspace.numel(), raw)
-            return t, c, r
-
-        return _run(self._dev, stream, call, out, workspace)
+        if _elsewhere(self._dev, stream):
+            with _launching(refs.device, stream):
+                return self.fork(block_tables, context_lens, refs, parents, children, out, workspace)
+        t, c, r = out if out is not None else (torch.empty_like(block_tables), torch.empty_like(context_lens),
+                                               torch.empty_like(refs))
+        if workspace is None:
+            workspace = torch.empty(tq_pages_fork_workspace_bytes(n), dtype=torch.uint8, device=refs.device)
+        tq_pages_fork(self._array, len(self._array), self.num_blocks, block_tables, t, context_lens, c, refs, r, rows,
+                      max_blocks, parents, children, n, workspace, workspace.numel(), _raw_stream(self._dev))
+        return t, c, r
 
     def compact(self, block_tables, refs, out=None, workspace=None, stream=None):
         """Move the used pages (refs > 0) to the front of the pools. Returns
@@ -775,7 +801,8 @@ class TQPagePools:
         import torch
 
         rows, max_blocks = _page_state(block_tables, None, refs, self.num_blocks)
-        _require(rows <= TQ_MAX_PAGE_ROWS, f"block_tables: at most {TQ_MAX_PAGE_ROWS} rows")
+        if rows > TQ_MAX_PAGE_ROWS:
+            raise ValueError(f"block_tables: at most {TQ_MAX_PAGE_ROWS} rows")
         if out is not None:
             _page_state(out[0], None, out[1], self.num_blocks)
             _require(out[0].shape == block_tables.shape, "out: tables of the same shape")
@@ -785,16 +812,14 @@ class TQPagePools:
             _check(workspace, "workspace", torch.uint8)
         self._on_mine(("block_tables", "refs", "workspace", "out", "out", "out", "out"),
                       (block_tables, refs, workspace, *(out if out is not None else ())))
-
-        def call(raw, out, workspace):
-            t, r, m, u = out if out is not None else (torch.empty_like(block_tables), torch.empty_like(refs),
-                                                      torch.empty_like(refs),
-                                                      torch.empty(1, dtype=torch.int32, device=refs.device))
-            if workspace is None:
-                workspace = torch.empty(tq_pages_compact_workspace_bytes(self.num_blocks), dtype=torch.uint8,
-                                        device=refs.device)
-            tq_pages_compact(self._array, len(self._array), self.num_blocks, block_tables, t, refs, r, rows,
-                             max_blocks, m, u, workspace, workspace.numel(), raw)
-            return t, r, m, u
-
-        return _run(self._dev, stream, call, out, workspace)
+        if _elsewhere(self._dev, stream):
+            with _launching(refs.device, stream):
+                return self.compact(block_tables, refs, out, workspace)
+        t, r, m, u = out if out is not None else (torch.empty_like(block_tables), torch.empty_like(refs),
+                                                  torch.empty_like(refs), refs.new_empty(1))
+        if workspace is None:
+            workspace = torch.empty(tq_pages_compact_workspace_bytes(self.num_blocks), dtype=torch.uint8,
+                                    device=refs.device)
+        tq_pages_compact(self._array, len(self._array), self.num_blocks, block_tables, t, refs, r, rows, max_blocks,
+                         m, u, workspace, workspace.numel(), _raw_stream(self._dev))
+        return t, r, m, u

@@ -354,12 +354,17 @@ __global__ void __launch_bounds__(PG_PLAN_THREADS) compact_count_kernel(const __
 __global__ void __launch_bounds__(PG_PLAN_THREADS) compact_plan_kernel(const __grid_constant__ PgCompact a) {
   __shared__ int buf[33];
   const int tid = threadIdx.x;
-  // used pages in all, and in the segments before this CTA's
+  // used pages in all, and in the segments before this CTA's (a single CTA
+  // counts them itself)
   int before_ = 0, all_ = 0;
-  for (int s = tid; s < a.segs; s += blockDim.x) {
-    const int v = a.seg_used[s];
-    all_ += v;
-    before_ += s < (int)blockIdx.x ? v : 0;
+  if (a.segs == 1) {
+    for (int64_t b = tid; b < a.num_blocks; b += blockDim.x) all_ += a.refs[b] > 0;
+  } else {
+    for (int s = tid; s < a.segs; s += blockDim.x) {
+      const int v = a.seg_used[s];
+      all_ += v;
+      before_ += s < (int)blockIdx.x ? v : 0;
+    }
   }
   int used, before;
   pg_scan(all_, buf, used);
@@ -574,8 +579,10 @@ tq_status tq_launch_pages_compact(const tq_page_pool* pools, int n_pools, int64_
   if (!a.err || cudaGetDevice(&dev) != cudaSuccess) return TQ_ERR_CUDA;
   const int sms = tq_sm_count(dev);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  compact_count_kernel<<<a.segs, PG_PLAN_THREADS, 0, st>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
+  if (a.segs > 1) {
+    compact_count_kernel<<<a.segs, PG_PLAN_THREADS, 0, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
+  }
   compact_plan_kernel<<<a.segs, PG_PLAN_THREADS, 0, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
   const PgPools p = make_pools(pools, n_pools);
