@@ -13,29 +13,35 @@
 //
 // This kernel is for few query rows per kv head (decode steps, drafted
 // tokens). A warp takes RT = 4 NT query rows of one kv head and one share of
-// the 16-position blocks that they see; warps of a CTA take neighbouring kv
-// heads of the same share, so their loads are neighbours in a cache row. Codes
-// go from global memory to registers (the next 32 positions' words are loaded
-// while the current ones are worked on), become fp16 pairs through
-// lane-replicated tables in shared memory (one conflict-free lookup per two
-// codes, four at 2-bit values) and are used NT times:
+// the 16-position blocks that they see; neighbouring warps take neighbouring
+// kv heads of the same share, whose cache rows are neighbours in memory. Each
+// warp copies its own tiles of 32 positions (codes and norms) into a private
+// ring in shared memory with asynchronous 4- to 16-byte copies and waits for
+// nobody. Codes become fp16 pairs through lane-replicated tables and are used
+// NT times:
 //  * scores: mma m16n8k16 with A = 16 positions x 16 dims of levels, B = 16
 //    dims x (4 rows x (hi, lo)) of the rotated query, whose fp16 value and
 //    remainder are added up in f32;
 //  * values: A = 16 dims x 16 positions of levels, B = 16 positions x (4 rows
 //    x (hi, lo)) of the weights, turned from the score layout by movmatrix.
+// Table entries are 256 bytes apart at a shared address that is a multiple of
+// 64 KB: the lookup's address is one byte permute that puts the index byte
+// over the lane's constant (128 bytes of key entries, then 128 of value
+// entries per index). An index byte is two 4-bit or four 2-bit key codes, one
+// 4-bit value code of two positions, or two 2-bit value codes of two
+// positions, so that a lookup returns whole operand registers; 3-bit codes
+// are looked up in pairs.
 //
 // Precision: sums, maxima and scores are f32. The fp16 operands are the levels
 // times a common factor that puts them within 2^-14 of fp16 values (host,
 // lev_f16), the rotated query as value + remainder (22 bits) scaled by a power
 // of two per row, and weight x norm as value + remainder, scaled by a power of
 // two that follows the largest value norm seen, so norms of any size neither
-// overflow nor vanish.
+// overflow nor vanish. The maximum that the weights refer to moves only when
+// it grows by more than 2^8 (exact: sum and accumulator share it).
 //
-// Bound: (P_K + P_V + 8) bytes per visible position and kv head against about
-// 30 warp instructions per block and kv head for each of lookups, MMAs and
-// softmax: like the decode-step kernel it issues at about half the rate that
-// HBM would allow.
+// Bound: (P_K + P_V + 8) bytes per visible position and kv head, against the
+// issue slots of about 500 warp instructions per 32 positions and kv head.
 #include <climits>
 #include <cmath>
 
@@ -43,41 +49,107 @@
 
 namespace tq {
 
-constexpr int AW_WARPS = 8;
-constexpr int AW_TILE = 32;  // positions per step: two blocks
+constexpr int AW_TILE = 32;             // positions per step: two blocks
+constexpr uint32_t AW_TABLE = 65536;    // bytes of the table, and its alignment
+constexpr int AW_SMEM = 232448;
 
-// Shared tables: pairs of codes -> two fp16 levels, one copy per lane; at
-// 2-bit values, four codes -> four levels, eight copies.
-template <int KB, int VB>
-struct AwTables {
-  static constexpr int K_BYTES = (1 << (2 * KB)) * 128;
-  static constexpr bool V_QUAD = VB == 2;
-  static constexpr int V_BYTES = V_QUAD ? 256 * 64 : (1 << (2 * VB)) * 128;
-  static constexpr int BYTES = K_BYTES + V_BYTES;
+template <int D, int KB, int VB, int NT>
+struct AwCfg {
+  static constexpr int PK = D * KB / 8, PV = D * VB / 8;
+  static constexpr int WARPS = D * NT <= 128 ? 16 : 8;  // by registers: 128 or 255 of a thread
+  static constexpr int CK = PK % 16 ? 8 : 16, CV = PV % 16 ? 8 : 16;  // bytes of a copy
+  static constexpr int K0 = 0, V0 = AW_TILE * PK, N0 = V0 + AW_TILE * PV;
+  static constexpr int STAGE = N0 + AW_TILE * 8;
+  // rings lie below and above the table; the dynamic region starts within 2 KB
+  // of shared address 0 (checked at run time)
+  static constexpr int BELOW = (int)AW_TABLE - 2048, ABOVE = AW_SMEM - 2 * (int)AW_TABLE;
+  static constexpr bool fits(int stages) {
+    return BELOW / (stages * STAGE) + ABOVE / (stages * STAGE) >= WARPS;
+  }
+  static constexpr int STAGES = fits(4) ? 4 : fits(3) ? 3 : 2;
+  static constexpr int RING = STAGES * STAGE;
+  static constexpr int LOW = BELOW / RING < WARPS ? BELOW / RING : WARPS;  // rings below the table
+  static_assert(fits(STAGES), "shared memory of the rings");
 };
 
-template <int KB, int VB>
-TQ_DEV void aw_build_tables(uint8_t* smem, const AwArgs& a) {
-  using T = AwTables<KB, VB>;
-  uint32_t* lk = reinterpret_cast<uint32_t*>(smem);
-  for (int e = threadIdx.x; e < T::K_BYTES / 4; e += blockDim.x) {
-    const int f = e >> 5;
-    lk[e] = a.k_lev[f & ((1 << KB) - 1)] | (uint32_t)a.k_lev[f >> KB] << 16;
-  }
-  if (T::V_QUAD) {
-    uint2* lv = reinterpret_cast<uint2*>(smem + T::K_BYTES);
-    for (int e = threadIdx.x; e < 256 * 8; e += blockDim.x) {
-      const int f = e >> 3;
-      lv[e] = make_uint2(a.v_lev[f & 3] | (uint32_t)a.v_lev[(f >> 2) & 3] << 16,
-                         a.v_lev[(f >> 4) & 3] | (uint32_t)a.v_lev[f >> 6] << 16);
+// Table entry of index f: operand words of the key half and of the value half.
+template <int KB>
+TQ_DEV uint2 aw_k_entry(const uint16_t* lev, int f) {
+  if (KB == 2)
+    return make_uint2(lev[f & 3] | (uint32_t)lev[(f >> 2) & 3] << 16,
+                      lev[(f >> 4) & 3] | (uint32_t)lev[(f >> 6) & 3] << 16);
+  const int m = (1 << KB) - 1;
+  return make_uint2(lev[f & m] | (uint32_t)lev[(f >> KB) & m] << 16, 0u);
+}
+template <int VB>
+TQ_DEV uint2 aw_v_entry(const uint16_t* lev, int f) {
+  if (VB == 2)  // two dims of one position (low nibble) and of the next (high)
+    return make_uint2(lev[f & 3] | (uint32_t)lev[(f >> 4) & 3] << 16,
+                      lev[(f >> 2) & 3] | (uint32_t)lev[(f >> 6) & 3] << 16);
+  const int m = (1 << VB) - 1;  // 4 bits: one dim of two positions; 3 bits: two dims
+  return make_uint2(lev[f & m] | (uint32_t)lev[(f >> VB) & m] << 16, 0u);
+}
+
+template <int BYTES>
+TQ_DEV void aw_copy(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+TQ_DEV void aw_copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+TQ_DEV void aw_copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+TQ_DEV uint2 lds64(uint32_t addr) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr));
+  return r;
+}
+
+// NBYTES bytes at shared address `addr` (a multiple of the largest power of
+// two up to 16 that divides NBYTES, at least 2; 3 bytes: any) as words; `end`
+// = first address behind the row, not read.
+template <int NBYTES, int NW>
+TQ_DEV void aw_lds(uint32_t (&w)[NW], uint32_t addr, uint32_t end) {
+  static_assert(NW == (NBYTES + 3) / 4, "words of the stream");
+  if constexpr (NBYTES % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < NBYTES / 16; ++i)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                   : "r"(addr + 16 * i));
+  } else if constexpr (NBYTES % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < NBYTES / 8; ++i) {
+      const uint2 r = lds64(addr + 8 * i);
+      w[2 * i] = r.x, w[2 * i + 1] = r.y;
     }
-  } else {
-    uint32_t* lv = reinterpret_cast<uint32_t*>(smem + T::K_BYTES);
-    for (int e = threadIdx.x; e < T::V_BYTES / 4; e += blockDim.x) {
-      const int f = e >> 5;
-      lv[e] = a.v_lev[f & ((1 << VB) - 1)] | (uint32_t)a.v_lev[f >> VB] << 16;
-    }
+  } else if constexpr (NBYTES % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < NBYTES / 4; ++i) w[i] = lds32(addr + 4 * i);
+  } else if constexpr (NBYTES == 2) {
+    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+  } else {  // 3 or 6 bytes: two aligned words
+    const uint32_t at = addr & ~3u, sh = (addr & 3u) * 8u;
+    const uint32_t r0 = lds32(at), r1 = lds32(min(at + 4u, end - 4u));
+    w[0] = __funnelshift_r(r0, r1, sh);
+    if constexpr (NW > 1) w[1] = r1 >> sh;
   }
+}
+
+// 16-byte chunk of a row in its ring slot: rows of 64 and 128 bytes are
+// swizzled so that the fragment loads of a warp fall in distinct banks. Value
+// rows go to slot (r % 2) 16 + r / 2 (a load's four rows are then neighbours).
+template <int P>
+TQ_DEV int aw_k_chunk(int row, int c) {
+  return P == 128 ? c ^ (row & 1) : c;
+}
+template <int P>
+TQ_DEV int aw_v_chunk(int slot, int c) {
+  return P == 64 ? c ^ (((slot >> 1) & 1) << 1) : P == 128 ? c ^ ((slot & 3) << 1) : c;
 }
 
 TQ_DEV uint32_t aw_transpose(uint32_t x) {
@@ -86,32 +158,113 @@ TQ_DEV uint32_t aw_transpose(uint32_t x) {
   return y;
 }
 
+// Address of the entry whose index is byte `i` of w.
+TQ_DEV uint32_t aw_at(uint32_t w, uint32_t lane_base, int i) { return __byte_perm(w, lane_base, 0x7604u | (i << 4)); }
+
 template <int D, int KB, int VB, int NT>
-__global__ void __launch_bounds__(AW_WARPS * 32, D == 256 || NT > 1 ? 1 : 2)
+__global__ void __launch_bounds__(AwCfg<D, KB, VB, NT>::WARPS * 32, 1)
     window_partial_kernel(const __grid_constant__ AwArgs a) {
-  constexpr int PK = D * KB / 8, PV = D * VB / 8;
+  using C = AwCfg<D, KB, VB, NT>;
+  constexpr int PK = C::PK, PV = C::PV, STAGES = C::STAGES, WARPS = C::WARPS;
   constexpr int KT = PK / 4, VT = PV / 8;  // bytes of a thread: a quarter of a K row, an eighth of a V row
   constexpr int KW = (KT + 3) / 4, VW = (VT + 3) / 4;
   constexpr int NB = D / 16;
-  constexpr int KF = 2 * KB, VF = 2 * VB;
   constexpr int RT = 4 * NT;
-  using Tab = AwTables<KB, VB>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, tq = lane & 3;
   const int b = blockIdx.z;
-  const int unit = blockIdx.x * AW_WARPS + warp;  // (split, kv head), heads fastest
+  const int unit = blockIdx.x * WARPS + warp;  // (split, kv head), heads fastest
   const int split = unit / a.hkv, hk = unit - split * a.hkv;
-  const bool live = split < a.n_split;
 
   const AwSeq sq = aw_sequence(a, b, blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0);
   const int rows = sq.n * a.g, r0 = blockIdx.y * RT;
   if (r0 >= rows) return;  // the whole CTA
-  aw_build_tables<KB, VB>(smem, a);
-  __syncthreads();
-  if (!live) return;
-  const uint32_t lutk = smem_u32(smem) + lane * 4u;
-  const uint32_t lutv = smem_u32(smem) + Tab::K_BYTES + (Tab::V_QUAD ? (lane & 7) * 8u : lane * 4u);
+  const uint32_t raw = smem_u32(smem);
+  if (raw > 2048u) {  // the rings would not lie where they were planned
+    if (threadIdx.x == 0) record_error(a.err, TQ_DEVERR_SMEM_LAYOUT);
+    return;
+  }
+  const uint32_t table = AW_TABLE;
+  const uint32_t ring = warp < C::LOW ? ((raw + 127u) & ~127u) + (uint32_t)(warp * C::RING)
+                                      : 2 * AW_TABLE + (uint32_t)((warp - C::LOW) * C::RING);
+
+  // ---- positions of this thread's score rows, the blocks of the tile, this split's share
+  int p_row[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int r = r0 + 4 * j + tq;
+    p_row[j] = r < rows ? aw_position(sq, r / a.g) : -1;
+  }
+  const int p_lo = aw_position(sq, r0 / a.g), p_hi = aw_position(sq, min(r0 + RT - 1, rows - 1) / a.g);
+  const AwBlocks bl = aw_blocks(p_lo, p_hi, a.window, a.sinks);
+  const int share = 2 * ((bl.n + 2 * a.n_split - 1) / (2 * a.n_split));
+  const int m0 = min(split * share, bl.n), m1 = split < a.n_split ? min(m0 + share, bl.n) : m0;
+  const int tiles = (m1 - m0 + 1) / 2;
+
+  // ---- copies of tile i into stage i % STAGES; rows behind the context come
+  // from its last row. Table entries are loaded one tile ahead.
+  int ent[2];
+  auto entries = [&](int i) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) ent[h] = aw_block_entry(a, b, aw_block(bl, min(m0 + 2 * i + h, m1 - 1)));
+  };
+  const int64_t k_step = (int64_t)a.hkv * PK, v_step = (int64_t)a.hkv * PV;
+  auto copy = [&](int i) {
+    const uint32_t st = ring + (uint32_t)((i % STAGES) * C::STAGE);
+    const uint8_t *kb[2], *vb[2];
+    int most[2];
+    int64_t row0[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = aw_block(bl, min(m0 + 2 * i + h, m1 - 1));
+      most[h] = sq.ctx - 1 - j * ATT_BLOCK;  // last row of the block inside the context
+      row0[h] = aw_entry_row(a, b, ent[h]) * a.hkv + hk;
+      kb[h] = a.k_packed + row0[h] * PK;
+      vb[h] = a.v_packed + row0[h] * PV;
+    }
+    constexpr int NK = PK / C::CK, NV = PV / C::CV;  // copies per row
+#pragma unroll
+    for (int it = 0; it < NK; ++it) {
+      const int e = it * 32 + lane, row = e / NK, c = e - row * NK;
+      const int h = row >> 4;
+      const uint8_t* src = (h ? kb[1] : kb[0]) + min(row & 15, h ? most[1] : most[0]) * k_step + c * C::CK;
+      aw_copy<C::CK>(st + C::K0 + row * PK + (C::CK == 16 ? aw_k_chunk<PK>(row, c) : c) * C::CK, src);
+    }
+#pragma unroll
+    for (int it = 0; it < NV; ++it) {
+      const int e = it * 32 + lane, row = e / NV, c = e - row * NV;
+      const int h = row >> 4, slot = (row & 1) * 16 + (row >> 1);
+      const uint8_t* src = (h ? vb[1] : vb[0]) + min(row & 15, h ? most[1] : most[0]) * v_step + c * C::CV;
+      aw_copy<C::CV>(st + C::V0 + slot * PV + (C::CV == 16 ? aw_v_chunk<PV>(slot, c) : c) * C::CV, src);
+    }
+    {
+      const int h = lane >> 4;
+      const int64_t n = (h ? row0[1] : row0[0]) + (int64_t)min(lane & 15, h ? most[1] : most[0]) * a.hkv;
+      aw_copy<4>(st + C::N0 + lane * 4, a.k_norms + n);
+      aw_copy<4>(st + C::N0 + 128 + lane * 4, a.v_norms + n);
+    }
+  };
+  if (tiles > 0) entries(0);
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) {
+    if (i < tiles) {
+      copy(i);
+      if (i + 1 < tiles) entries(i + 1);
+    }
+    aw_copy_commit();
+  }
+
+  // ---- the table: 8 threads per index, each 32 bytes of its two halves' copies
+  for (int e = threadIdx.x; e < 256 * 16; e += WARPS * 32) {
+    const int f = e >> 4, part = e & 15;  // 16 bytes each: 8 of keys, 8 of values
+    const uint2 w = part < 8 ? aw_k_entry<KB>(a.k_lev, f) : aw_v_entry<VB>(a.v_lev, f);
+    const bool two = part < 8 ? KB == 2 : VB == 2;
+    const uint4 v = two ? make_uint4(w.x, w.y, w.x, w.y) : make_uint4(w.x, w.x, w.x, w.x);
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(table + (uint32_t)(f * 256 + part * 16)), "r"(v.x),
+                 "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+  }
 
   // ---- rotated queries: this lane's quarter of the row of its B column
   uint32_t bq[NT][NB][2];
@@ -175,154 +328,162 @@ __global__ void __launch_bounds__(AW_WARPS * 32, D == 256 || NT > 1 ? 1 : 2)
         bq[j][kb][e2] = pack_half2(v0, v1);
       }
   }
+  __syncthreads();  // the table is complete
+  if (split >= a.n_split) return;
 
-  // ---- positions of this thread's score rows, and the blocks of the tile
-  int p_row[NT];
+  const uint32_t lut_k = table + (KB == 2 ? (lane & 15) * 8u : lane * 4u);
+  const uint32_t lut_v = table + 128u + (VB == 2 ? (lane & 15) * 8u : lane * 4u);
+  float m_ref[NT], l_run[NT], acc[NT][NB][4];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int r = r0 + 4 * j + tq;
-    p_row[j] = r < rows ? aw_position(sq, r / a.g) : -1;
-  }
-  const int p_lo = aw_position(sq, r0 / a.g), p_hi = aw_position(sq, min(r0 + RT - 1, rows - 1) / a.g);
-  const AwBlocks bl = aw_blocks(p_lo, p_hi, a.window, a.sinks);
-  const int share = 2 * ((bl.n + 2 * a.n_split - 1) / (2 * a.n_split));
-  const int m0 = split * share, m1 = min(m0 + share, bl.n);
-
-  float m_run[NT], l_run[NT], acc[NT][NB][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    m_run[j] = -INFINITY;
+    m_ref[j] = -INFINITY;
     l_run[j] = 0.f;
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[j][i][c] = 0.f;
   }
-  // weights are held times 2^10 / (a power of two near the largest value norm)
-  float v_up = 1.f, v_inv = 1.f, v_most = 0.f;
+  // value norms times v_up lie below 64; v_up is 2^5 over a power of two near
+  // the largest one seen
+  float v_up = 0.f, v_inv = 1.f;
 
-  // one step's codes and norms; rows behind the context are read from its last row
-  uint32_t kw[2][2][KW], vw[2][4][VW];
-  float nk[2][2], nv[2][2];
-  int t_blk[2];
-  auto fetch = [&](int m) {
+  for (int i = 0; i < tiles; ++i) {
+    aw_copy_wait<STAGES - 2>();
+    __syncwarp();  // every lane's copies of this tile are there, and the stage before it is free
+    if (i + STAGES - 1 < tiles) {
+      copy(i + STAGES - 1);
+      if (i + STAGES < tiles) entries(i + STAGES);
+    }
+    aw_copy_commit();
+    const uint32_t st = ring + (uint32_t)((i % STAGES) * C::STAGE);
+    int t_blk[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      t_blk[h] = m0 + 2 * i + h < m1 ? aw_block(bl, m0 + 2 * i + h) * ATT_BLOCK : INT_MAX - 64;  // behind every query
+    bool hidden = false;  // some position is masked for some row
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int j = aw_block(bl, min(m + h, m1 - 1));
-      t_blk[h] = m + h < m1 ? j * ATT_BLOCK : INT_MAX - 64;  // behind every query
-      const int64_t base = aw_block_row(a, b, j);
-      const int most = sq.ctx - 1 - j * ATT_BLOCK;  // last row of the block inside the context
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int64_t row = (base + min(gq + 8 * r, most)) * a.hkv + hk;
-        aw_load<KT, KW>(kw[h][r], a.k_packed + row * PK, tq * KT, PK);
-        nk[h][r] = __ldg(a.k_norms + row);
-        nv[h][r] = __ldg(a.v_norms + row);
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t row = (base + min(2 * tq + (r & 1) + 8 * (r >> 1), most)) * a.hkv + hk;
-        aw_load<VT, VW>(vw[h][r], a.v_packed + row * PV, gq * VT, PV);
-      }
+      const int t1 = t_blk[h] + ATT_BLOCK - 1;
+      hidden = hidden || !(t1 <= p_lo && (t1 < a.sinks || t_blk[h] > p_hi - a.window));
     }
-  };
-  if (m0 < m1) fetch(m0);
-
-  for (int m = m0; m < m1; m += 2) {
-    uint32_t ck[2][2][KW], cv[2][4][VW];
-    float cnk[2][2], cnv[2][2];
-    int ct[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      ct[h] = t_blk[h];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        cnk[h][r] = nk[h][r];
-        cnv[h][r] = nv[h][r];
-#pragma unroll
-        for (int i = 0; i < KW; ++i) ck[h][r][i] = kw[h][r][i];
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int i = 0; i < VW; ++i) cv[h][r][i] = vw[h][r][i];
-    }
-    if (m + 2 < m1) fetch(m + 2);
 
     // ---- scores
-    float sc[NT][2][2];
+    float sc[NT][2][2], nv[2][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float c[NT][4];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[j][i] = 0.f;
+        for (int q = 0; q < 4; ++q) c[j][q] = 0.f;
+      uint32_t w0[KW], w1[KW];
+      const int ra = 16 * h + gq;
+      if constexpr (PK == 128) {  // two swizzled chunks of 16 bytes
+#pragma unroll
+        for (int q = 0; q < KT / 16; ++q) {
+          uint32_t u[4];
+          const uint32_t at = st + C::K0 + ra * PK + aw_k_chunk<PK>(ra, tq * (KT / 16) + q) * 16;
+          aw_lds<16>(u, at, 0);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) w0[4 * q + z] = u[z];
+          aw_lds<16>(u, at + 8 * PK, 0);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) w1[4 * q + z] = u[z];
+        }
+      } else {
+        const uint32_t row = st + C::K0 + ra * PK;
+        aw_lds<KT>(w0, row + tq * KT, row + PK);
+        aw_lds<KT>(w1, row + 8 * PK + tq * KT, row + 9 * PK);
+      }
 #pragma unroll
       for (int kb = 0; kb < NB; ++kb) {
-        const uint32_t a0 = lds32(aw_bits<KF>(ck[h][0], 2 * kb * KF) * 128u + lutk);
-        const uint32_t a1 = lds32(aw_bits<KF>(ck[h][1], 2 * kb * KF) * 128u + lutk);
-        const uint32_t a2 = lds32(aw_bits<KF>(ck[h][0], (2 * kb + 1) * KF) * 128u + lutk);
-        const uint32_t a3 = lds32(aw_bits<KF>(ck[h][1], (2 * kb + 1) * KF) * 128u + lutk);
+        uint32_t a0, a1, a2, a3;
+        if constexpr (KB == 4) {
+          a0 = lds32(aw_at(w0[kb / 2], lut_k, 2 * (kb & 1)));
+          a1 = lds32(aw_at(w1[kb / 2], lut_k, 2 * (kb & 1)));
+          a2 = lds32(aw_at(w0[kb / 2], lut_k, 2 * (kb & 1) + 1));
+          a3 = lds32(aw_at(w1[kb / 2], lut_k, 2 * (kb & 1) + 1));
+        } else if constexpr (KB == 2) {
+          const uint2 u = lds64(aw_at(w0[kb / 4], lut_k, kb & 3)), v = lds64(aw_at(w1[kb / 4], lut_k, kb & 3));
+          a0 = u.x, a2 = u.y, a1 = v.x, a3 = v.y;
+        } else {
+          a0 = lds32(aw_bits<6>(w0, 12 * kb) * 256u + lut_k);
+          a1 = lds32(aw_bits<6>(w1, 12 * kb) * 256u + lut_k);
+          a2 = lds32(aw_bits<6>(w0, 12 * kb + 6) * 256u + lut_k);
+          a3 = lds32(aw_bits<6>(w1, 12 * kb + 6) * 256u + lut_k);
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j) mma16816(c[j], a0, a1, a2, a3, bq[j][kb][0], bq[j][kb][1]);
       }
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int r = 0; r < 2; ++r) {
+        const float nk = __uint_as_float(lds32(st + C::N0 + (ra + 8 * r) * 4));
+        nv[h][r] = __uint_as_float(lds32(st + C::N0 + 128 + (ra + 8 * r) * 4));
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sc[j][h][r] = (c[j][2 * r] + c[j][2 * r + 1]) * (nk * row_inv[j]);
+      }
+    }
+    if (hidden) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const bool see = aw_visible(ct[h] + gq + 8 * r, p_row[j], a.window, a.sinks);
-          sc[j][h][r] = see ? (c[j][2 * r] + c[j][2 * r + 1]) * (cnk[h][r] * row_inv[j]) : -INFINITY;
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            if (!aw_visible(t_blk[h] + gq + 8 * r, p_row[j], a.window, a.sinks)) sc[j][h][r] = -INFINITY;
+          // a norm that no row sees takes no part (it may be infinite or NaN)
+          if (t_blk[h] + gq + 8 * r > p_hi) nv[h][r] = 0.f;
         }
     }
-    // ---- the power of two of the weights: follows the largest value norm
-    float nmax = 0.f;
+    // ---- a larger value norm than any before moves their power of two
+    float fix_all = 1.f;
+    {
+      float most = 0.f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float v = fabsf(cnv[h][r]);
-        if (ct[h] + gq + 8 * r <= p_hi && v < INFINITY) nmax = fmaxf(nmax, v);
+        for (int r = 0; r < 2; ++r) {
+          const float v = fabsf(nv[h][r]);
+          if (v < INFINITY) most = fmaxf(most, v);
+        }
+      if (__any_sync(0xffffffffu, v_up == 0.f ? most > 0.f : most * v_up >= 64.f)) {
+        most = fmaxf(warp_max8(most), v_up == 0.f ? 0.f : 32.f * v_inv);  // at least the power of two so far
+        float inv;
+        const float up = aw_pow2_for<5>(most, inv);
+        fix_all = v_up == 0.f ? 1.f : up * v_inv;
+        v_up = up;
+        v_inv = inv;
       }
-    nmax = warp_max8(nmax);
-    float v_fix = 1.f;
-    if (nmax > v_most) {
-      v_most = nmax;
-      float inv;
-      const float up = aw_pow2_for<10>(nmax, inv);
-      v_fix = up * v_inv;  // <= 1 from the second time on
-      v_up = up;
-      v_inv = inv;
     }
-    // ---- running maximum and sum; weights times norms as value + remainder
+    // ---- reference maxima and sums; weights times norms as value + remainder
     uint32_t bp[NT][2][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const float mx = warp_max8(fmaxf(fmaxf(sc[j][0][0], sc[j][0][1]), fmaxf(sc[j][1][0], sc[j][1][1])));
-      const float mn = fmaxf(m_run[j], mx);
-      const float ref = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every weight is exp2(-inf) = 0
-      const float alpha = aw_exp2(m_run[j] - ref);
-      float p[2][2], sum = 0.f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          p[h][r] = aw_exp2(sc[j][h][r] - ref);
-          sum += p[h][r];
+      const bool move = mx > m_ref[j] + 8.0f;  // from -inf by any score
+      if (__any_sync(0xffffffffu, move || fix_all != 1.f)) {
+        float fix = fix_all;
+        if (move) {
+          const float f = aw_exp2(m_ref[j] - mx);
+          l_run[j] *= f;
+          fix *= f;
+          m_ref[j] = mx;
         }
-      l_run[j] = l_run[j] * alpha + sum;  // of this lane's positions
-      m_run[j] = mn;
-      // the accumulator's columns 2 tq, 2 tq + 1 belong to this same row
-      const float fix = alpha * v_fix;
+        // (the accumulator's columns 2 tq, 2 tq + 1 belong to this same row)
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+        for (int q = 0; q < NB; ++q)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[j][i][c] *= fix;
+          for (int c = 0; c < 4; ++c) acc[j][q][c] *= fix;
+      }
+      const float ref = m_ref[j] == -INFINITY ? 0.f : m_ref[j];  // nothing seen yet: weights exp2(-inf) = 0
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float w = sc[j][h][r] == -INFINITY ? 0.f : p[h][r] * (cnv[h][r] * v_up);
+          const float p = aw_exp2(sc[j][h][r] - ref);
+          l_run[j] += p;  // of this lane's positions
+          float w = p * (nv[h][r] * v_up);
+          if (hidden && sc[j][h][r] == -INFINITY) w = 0.f;  // whatever the norm is
           const float hi = __half2float(__float2half_rn(w));
           bp[j][h][r] = aw_transpose(pack_half2(hi, w - hi));
         }
@@ -330,36 +491,55 @@ __global__ void __launch_bounds__(AW_WARPS * 32, D == 256 || NT > 1 ? 1 : 2)
     // ---- values
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (Tab::V_QUAD) {
+      uint32_t w[4][VW];
 #pragma unroll
-        for (int i = 0; i < NB / 2; ++i) {
-          uint2 lv[4];
+      for (int q = 0; q < 4; ++q) {  // positions 2 tq, 2 tq + 1, + 8, + 9 of the block
+        const int row = 16 * h + 2 * tq + (q & 1) + 8 * (q >> 1), slot = (row & 1) * 16 + (row >> 1);
+        const uint32_t at = st + C::V0 + slot * PV;
+        if constexpr (PV == 64 || PV == 128) {
+          constexpr int PER = PV == 64 ? 2 : 1;  // threads sharing a 16-byte chunk
+          aw_lds<VT>(w[q], at + aw_v_chunk<PV>(slot, gq / PER) * 16 + (gq % PER) * VT, 0);
+        } else {
+          aw_lds<VT>(w[q], at + gq * VT, at + PV);
+        }
+      }
+      auto product = [&](int mb, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                         : "=r"(lv[r].x), "=r"(lv[r].y)
-                         : "r"(aw_bits<8>(cv[h][r], 8 * i) * 64u + lutv));
+        for (int j = 0; j < NT; ++j) mma16816(acc[j][mb], a0, a1, a2, a3, bp[j][h][0], bp[j][h][1]);
+      };
+      if constexpr (VB == 3) {
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const uint32_t l0 = s ? lv[0].y : lv[0].x, l1 = s ? lv[1].y : lv[1].x;
-            const uint32_t l2 = s ? lv[2].y : lv[2].x, l3 = s ? lv[3].y : lv[3].x;
-            const uint32_t a0 = __byte_perm(l0, l1, 0x5410), a1 = __byte_perm(l0, l1, 0x7632);
-            const uint32_t a2 = __byte_perm(l2, l3, 0x5410), a3 = __byte_perm(l2, l3, 0x7632);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) mma16816(acc[j][2 * i + s], a0, a1, a2, a3, bp[j][h][0], bp[j][h][1]);
-          }
+        for (int mb = 0; mb < NB; ++mb) {
+          const uint32_t l0 = lds32(aw_bits<6>(w[0], 6 * mb) * 256u + lut_v);
+          const uint32_t l1 = lds32(aw_bits<6>(w[1], 6 * mb) * 256u + lut_v);
+          const uint32_t l2 = lds32(aw_bits<6>(w[2], 6 * mb) * 256u + lut_v);
+          const uint32_t l3 = lds32(aw_bits<6>(w[3], 6 * mb) * 256u + lut_v);
+          product(mb, __byte_perm(l0, l1, 0x5410), __byte_perm(l0, l1, 0x7632), __byte_perm(l2, l3, 0x5410),
+                  __byte_perm(l2, l3, 0x7632));
         }
       } else {
+        // index bytes: a nibble of one position with the same nibble of the
+        // next (low nibbles of every byte, then high ones)
+        constexpr uint32_t LOWS = 0x0f0f0f0fu;
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          const uint32_t l0 = lds32(aw_bits<VF>(cv[h][0], i * VF) * 128u + lutv);
-          const uint32_t l1 = lds32(aw_bits<VF>(cv[h][1], i * VF) * 128u + lutv);
-          const uint32_t l2 = lds32(aw_bits<VF>(cv[h][2], i * VF) * 128u + lutv);
-          const uint32_t l3 = lds32(aw_bits<VF>(cv[h][3], i * VF) * 128u + lutv);
-          const uint32_t a0 = __byte_perm(l0, l1, 0x5410), a1 = __byte_perm(l0, l1, 0x7632);
-          const uint32_t a2 = __byte_perm(l2, l3, 0x5410), a3 = __byte_perm(l2, l3, 0x7632);
+        for (int z = 0; z < VW; ++z) {
+          const uint32_t e0 = (w[0][z] & LOWS) | ((w[1][z] << 4) & ~LOWS);
+          const uint32_t o0 = ((w[0][z] >> 4) & LOWS) | (w[1][z] & ~LOWS);
+          const uint32_t e1 = (w[2][z] & LOWS) | ((w[3][z] << 4) & ~LOWS);
+          const uint32_t o1 = ((w[2][z] >> 4) & LOWS) | (w[3][z] & ~LOWS);
+          constexpr int BY = VT < 4 ? VT : 4;  // bytes of a word
 #pragma unroll
-          for (int j = 0; j < NT; ++j) mma16816(acc[j][i], a0, a1, a2, a3, bp[j][h][0], bp[j][h][1]);
+          for (int y = 0; y < BY; ++y) {
+            if constexpr (VB == 2) {  // nibble = two dims: an M-block per nibble
+              const uint2 u = lds64(aw_at(e0, lut_v, y)), v = lds64(aw_at(e1, lut_v, y));
+              product(8 * z + 2 * y, u.x, u.y, v.x, v.y);
+              const uint2 s = lds64(aw_at(o0, lut_v, y)), t = lds64(aw_at(o1, lut_v, y));
+              product(8 * z + 2 * y + 1, s.x, s.y, t.x, t.y);
+            } else {  // nibble = one dim: an M-block per byte
+              product(4 * z + y, lds32(aw_at(e0, lut_v, y)), lds32(aw_at(o0, lut_v, y)), lds32(aw_at(e1, lut_v, y)),
+                      lds32(aw_at(o1, lut_v, y)));
+            }
+          }
         }
       }
     }
@@ -383,10 +563,10 @@ __global__ void __launch_bounds__(AW_WARPS * 32, D == 256 || NT > 1 ? 1 : 2)
       if (ok) {
         const int64_t idx = out_row * a.n_split + split;
         if (gq == 0) {
-          a.ws_m[idx] = m_run[j];
+          a.ws_m[idx] = m_ref[j];
           a.ws_l[idx] = l;
         }
-        if (m_run[j] != -INFINITY) {
+        if (m_ref[j] != -INFINITY) {
           float4* dst = reinterpret_cast<float4*>(a.ws_acc + idx * D + gq * (D / 8));
 #pragma unroll
           for (int e = 0; e < D / 8; e += 4)
@@ -395,7 +575,7 @@ __global__ void __launch_bounds__(AW_WARPS * 32, D == 256 || NT > 1 ? 1 : 2)
       }
       continue;
     }
-    const float inv = l > 0.f ? v_inv * a.o_scale / l : 0.f;
+    const float inv = l > 0.f ? v_inv * a.o_scale / l : (l == l ? 0.f : l);  // NaN where the sum is
 #pragma unroll
     for (int h = 1; h < D / 8; h <<= 1)
 #pragma unroll
@@ -499,7 +679,7 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_consta
 }
 
 // Query rows per kv head from which the tensor-memory kernel takes a call.
-constexpr int64_t AW_TC_ROWS = 32;
+constexpr int64_t AW_TC_ROWS = 64;
 
 static bool window_tc(int hq, int hkv, int max_q) { return (int64_t)max_q * (hq / hkv) >= AW_TC_ROWS; }
 
@@ -509,26 +689,27 @@ static bool window_tc(int hq, int hkv, int max_q) { return (int64_t)max_q * (hq 
 // tiles of 64 each.
 static int window_splits(int B, int hq, int hkv, int max_q, int d, int64_t s_max, int64_t window, int64_t sinks) {
   const bool tc = window_tc(hq, hkv, max_q);
-  const int64_t rt = tc ? tq_window_tc_rows(d) : 4;
-  const int64_t tiles = ((int64_t)max_q * (hq / hkv) + rt - 1) / rt;
+  const int64_t rows = (int64_t)max_q * (hq / hkv);
+  const int64_t rt = tc ? tq_window_tc_rows(d) : rows > 4 && d <= 128 ? 8 : 4;
+  const int64_t tiles = (rows + rt - 1) / rt;
   const int64_t units = (int64_t)B * hkv * tiles;
   int64_t seen = s_max;
   if (window > 0) seen = std::min(seen, window + sinks + max_q + 2 * ATT_BLOCK);
   const int64_t steps = tc ? (seen + 255) / 256 : (seen + AW_TILE - 1) / AW_TILE;
-  const int64_t slots = tc ? 148 : (d == 256 ? 1 : 2) * 148 * AW_WARPS;
+  const int64_t slots = tc ? 148 : 148 * (d * rt <= 512 ? 16 : 8);
   return (int)std::max<int64_t>(1, std::min<int64_t>(slots / units, steps));
 }
 
 template <int D, int KB, int VB, int NT>
 static cudaError_t launch_window_t(const AwArgs& a, cudaStream_t st) {
-  constexpr int smem = AwTables<KB, VB>::BYTES;
+  using C = AwCfg<D, KB, VB, NT>;
   cudaError_t e = cudaFuncSetAttribute(window_partial_kernel<D, KB, VB, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, AW_SMEM);
   if (e != cudaSuccess) return e;
-  const int64_t gx = ((int64_t)a.n_split * a.hkv + AW_WARPS - 1) / AW_WARPS;
+  const int64_t gx = ((int64_t)a.n_split * a.hkv + C::WARPS - 1) / C::WARPS;
   const int64_t gy = ((int64_t)a.max_q * a.g + 4 * NT - 1) / (4 * NT);
   if (gx > 0x7fffffff || gy > 65535) return cudaErrorNotSupported;
-  window_partial_kernel<D, KB, VB, NT><<<dim3((unsigned)gx, (unsigned)gy, a.B), AW_WARPS * 32, smem, st>>>(a);
+  window_partial_kernel<D, KB, VB, NT><<<dim3((unsigned)gx, (unsigned)gy, a.B), C::WARPS * 32, AW_SMEM, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.n_split == 1) return e;
   return tq_launch_window_combine(a, D, st);
