@@ -171,13 +171,17 @@ __global__ void __launch_bounds__(AwCfg<D, KB, VB, NT>::WARPS * 32, 1)
   constexpr int NB = D / 16;
   constexpr int RT = 4 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // what is the same for a warp is broadcast from its first lane: the compiler
+  // then keeps what follows from it (blocks, addresses) in uniform registers
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int gq = lane >> 2, tq = lane & 3;
   const int b = blockIdx.z;
   const int unit = blockIdx.x * WARPS + warp;  // (split, kv head), heads fastest
   const int split = unit / a.hkv, hk = unit - split * a.hkv;
 
-  const AwSeq sq = aw_sequence(a, b, blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0);
+  AwSeq sq = aw_sequence(a, b, blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0);
+  sq.n = __shfl_sync(0xffffffffu, sq.n, 0);
+  sq.ctx = __shfl_sync(0xffffffffu, sq.ctx, 0);
   const int rows = sq.n * a.g, r0 = blockIdx.y * RT;
   if (r0 >= rows) return;  // the whole CTA
   const uint32_t raw = smem_u32(smem);
@@ -202,48 +206,78 @@ __global__ void __launch_bounds__(AwCfg<D, KB, VB, NT>::WARPS * 32, 1)
   const int m0 = min(split * share, bl.n), m1 = split < a.n_split ? min(m0 + share, bl.n) : m0;
   const int tiles = (m1 - m0 + 1) / 2;
 
-  // ---- copies of tile i into stage i % STAGES; rows behind the context come
-  // from its last row. Table entries are loaded one tile ahead.
+  // ---- copies of tile i into stage i % STAGES; rows behind the context are
+  // read from its last one. Table entries are loaded one tile ahead.
   int ent[2];
   auto entries = [&](int i) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) ent[h] = aw_block_entry(a, b, aw_block(bl, min(m0 + 2 * i + h, m1 - 1)));
+    for (int h = 0; h < 2; ++h)
+      ent[h] = __shfl_sync(0xffffffffu, aw_block_entry(a, b, aw_block(bl, min(m0 + 2 * i + h, m1 - 1))), 0);
   };
-  const int64_t k_step = (int64_t)a.hkv * PK, v_step = (int64_t)a.hkv * PV;
+  constexpr int NK = PK / C::CK, NV = PV / C::CV;  // copies per row; as many per lane
+  const int k_step = a.hkv * PK, v_step = a.hkv * PV;
+  // offsets of this lane's copies within a block that is whole
+  int k_off[NK], v_off[NV];
+#pragma unroll
+  for (int it = 0; it < NK; ++it) {
+    const int e = it * 32 + lane, row = e / NK;
+    k_off[it] = (row & 15) * k_step + (e - row * NK) * C::CK;
+  }
+#pragma unroll
+  for (int it = 0; it < NV; ++it) {
+    const int e = it * 32 + lane, row = e / NV;
+    v_off[it] = (row & 15) * v_step + (e - row * NV) * C::CV;
+  }
   auto copy = [&](int i) {
     const uint32_t st = ring + (uint32_t)((i % STAGES) * C::STAGE);
     const uint8_t *kb[2], *vb[2];
-    int most[2];
     int64_t row0[2];
+    int over = 0;  // rows of the last block behind the context
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int j = aw_block(bl, min(m0 + 2 * i + h, m1 - 1));
-      most[h] = sq.ctx - 1 - j * ATT_BLOCK;  // last row of the block inside the context
       row0[h] = aw_entry_row(a, b, ent[h]) * a.hkv + hk;
       kb[h] = a.k_packed + row0[h] * PK;
       vb[h] = a.v_packed + row0[h] * PV;
+      over = max(over, (aw_block(bl, min(m0 + 2 * i + h, m1 - 1)) + 1) * ATT_BLOCK - sq.ctx);
     }
-    constexpr int NK = PK / C::CK, NV = PV / C::CV;  // copies per row
+    const int n_row = lane & 15;
+    int64_t n = row0[0] + (int64_t)n_row * a.hkv;
+    if (lane >= 16) n = row0[1] + (int64_t)n_row * a.hkv;
+    if (over <= 0) {
 #pragma unroll
-    for (int it = 0; it < NK; ++it) {
-      const int e = it * 32 + lane, row = e / NK, c = e - row * NK;
-      const int h = row >> 4;
-      const uint8_t* src = (h ? kb[1] : kb[0]) + min(row & 15, h ? most[1] : most[0]) * k_step + c * C::CK;
-      aw_copy<C::CK>(st + C::K0 + row * PK + (C::CK == 16 ? aw_k_chunk<PK>(row, c) : c) * C::CK, src);
-    }
+      for (int it = 0; it < NK; ++it) {
+        const int e = it * 32 + lane, row = e / NK, c = e - row * NK;
+        aw_copy<C::CK>(st + C::K0 + row * PK + (C::CK == 16 ? aw_k_chunk<PK>(row, c) : c) * C::CK,
+                       (row < 16 ? kb[0] : kb[1]) + k_off[it]);
+      }
 #pragma unroll
-    for (int it = 0; it < NV; ++it) {
-      const int e = it * 32 + lane, row = e / NV, c = e - row * NV;
-      const int h = row >> 4, slot = (row & 1) * 16 + (row >> 1);
-      const uint8_t* src = (h ? vb[1] : vb[0]) + min(row & 15, h ? most[1] : most[0]) * v_step + c * C::CV;
-      aw_copy<C::CV>(st + C::V0 + slot * PV + (C::CV == 16 ? aw_v_chunk<PV>(slot, c) : c) * C::CV, src);
-    }
-    {
+      for (int it = 0; it < NV; ++it) {
+        const int e = it * 32 + lane, row = e / NV, c = e - row * NV, slot = (row & 1) * 16 + (row >> 1);
+        aw_copy<C::CV>(st + C::V0 + slot * PV + (C::CV == 16 ? aw_v_chunk<PV>(slot, c) : c) * C::CV,
+                       (row < 16 ? vb[0] : vb[1]) + v_off[it]);
+      }
+    } else {
+      int most[2];  // last row of each block inside the context
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        most[h] = min(15, sq.ctx - 1 - aw_block(bl, min(m0 + 2 * i + h, m1 - 1)) * ATT_BLOCK);
+#pragma unroll 1
+      for (int e = lane; e < 32 * NK; e += 32) {
+        const int row = e / NK, c = e - row * NK, h = row >> 4;
+        aw_copy<C::CK>(st + C::K0 + row * PK + (C::CK == 16 ? aw_k_chunk<PK>(row, c) : c) * C::CK,
+                       (h ? kb[1] : kb[0]) + min(row & 15, h ? most[1] : most[0]) * k_step + c * C::CK);
+      }
+#pragma unroll 1
+      for (int e = lane; e < 32 * NV; e += 32) {
+        const int row = e / NV, c = e - row * NV, h = row >> 4, slot = (row & 1) * 16 + (row >> 1);
+        aw_copy<C::CV>(st + C::V0 + slot * PV + (C::CV == 16 ? aw_v_chunk<PV>(slot, c) : c) * C::CV,
+                       (h ? vb[1] : vb[0]) + min(row & 15, h ? most[1] : most[0]) * v_step + c * C::CV);
+      }
       const int h = lane >> 4;
-      const int64_t n = (h ? row0[1] : row0[0]) + (int64_t)min(lane & 15, h ? most[1] : most[0]) * a.hkv;
-      aw_copy<4>(st + C::N0 + lane * 4, a.k_norms + n);
-      aw_copy<4>(st + C::N0 + 128 + lane * 4, a.v_norms + n);
+      n = (h ? row0[1] : row0[0]) + (int64_t)min(n_row, h ? most[1] : most[0]) * a.hkv;
     }
+    aw_copy<4>(st + C::N0 + lane * 4, a.k_norms + n);
+    aw_copy<4>(st + C::N0 + 128 + lane * 4, a.v_norms + n);
   };
   if (tiles > 0) entries(0);
 #pragma unroll
@@ -360,12 +394,8 @@ __global__ void __launch_bounds__(AwCfg<D, KB, VB, NT>::WARPS * 32, 1)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       t_blk[h] = m0 + 2 * i + h < m1 ? aw_block(bl, m0 + 2 * i + h) * ATT_BLOCK : INT_MAX - 64;  // behind every query
-    bool hidden = false;  // some position is masked for some row
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int t1 = t_blk[h] + ATT_BLOCK - 1;
-      hidden = hidden || !(t1 <= p_lo && (t1 < a.sinks || t_blk[h] > p_hi - a.window));
-    }
+    // whether some position may be masked for some row (also in the sinks' blocks)
+    const bool hidden = t_blk[0] <= p_hi - a.window || t_blk[1] + (ATT_BLOCK - 1) > p_lo;
 
     // ---- scores
     float sc[NT][2][2], nv[2][2];
@@ -438,21 +468,24 @@ __global__ void __launch_bounds__(AwCfg<D, KB, VB, NT>::WARPS * 32, 1)
     // ---- a larger value norm than any before moves their power of two
     float fix_all = 1.f;
     {
-      float most = 0.f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float v = fabsf(nv[h][r]);
-          if (v < INFINITY) most = fmaxf(most, v);
-        }
+      float most = fmaxf(fmaxf(fabsf(nv[0][0]), fabsf(nv[0][1])), fmaxf(fabsf(nv[1][0]), fabsf(nv[1][1])));
       if (__any_sync(0xffffffffu, v_up == 0.f ? most > 0.f : most * v_up >= 64.f)) {
+        most = 0.f;  // the largest finite one
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float v = fabsf(nv[h][r]);
+            if (v < INFINITY) most = fmaxf(most, v);
+          }
         most = fmaxf(warp_max8(most), v_up == 0.f ? 0.f : 32.f * v_inv);  // at least the power of two so far
-        float inv;
-        const float up = aw_pow2_for<5>(most, inv);
-        fix_all = v_up == 0.f ? 1.f : up * v_inv;
-        v_up = up;
-        v_inv = inv;
+        if (most > 0.f) {
+          float inv;
+          const float up = aw_pow2_for<5>(most, inv);
+          fix_all = v_up == 0.f ? 1.f : up * v_inv;
+          v_up = up;
+          v_inv = inv;
+        }
       }
     }
     // ---- reference maxima and sums; weights times norms as value + remainder
@@ -639,15 +672,22 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_consta
       }
       const int n = min(32, a.n_split - s0);
       const float* acc = a.ws_acc + (row * a.n_split + s0) * D + lane * E;
-#pragma unroll 4
-      for (int s = 0; s < n; ++s) {
-        const float ws = __shfl_sync(0xffffffffu, w, s);
-        if (ws == 0.f) continue;  // an empty split has written no accumulator
+      for (int s1 = 0; s1 < n; s1 += 8) {  // eight splits' loads in flight
+        float v[8][E];
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 v = *reinterpret_cast<const float2*>(acc + (int64_t)s * D + e);
-          x[e] = fmaf(ws, v.x, x[e]);
-          x[e + 1] = fmaf(ws, v.y, x[e + 1]);
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const float2 u = s1 + k < n ? *reinterpret_cast<const float2*>(acc + (int64_t)(s1 + k) * D + e)
+                                        : make_float2(0.f, 0.f);
+            v[k][e] = u.x, v[k][e + 1] = u.y;
+          }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float ws = __shfl_sync(0xffffffffu, w, (s1 + k) & 31);
+          const bool some = s1 + k < n && ws != 0.f;  // an empty split has written no accumulator
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[e] = some ? fmaf(ws, v[k][e], x[e]) : x[e];
         }
       }
     }
@@ -679,7 +719,7 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_consta
 }
 
 // Query rows per kv head from which the tensor-memory kernel takes a call.
-constexpr int64_t AW_TC_ROWS = 64;
+constexpr int64_t AW_TC_ROWS = 16;
 
 static bool window_tc(int hq, int hkv, int max_q) { return (int64_t)max_q * (hq / hkv) >= AW_TC_ROWS; }
 

@@ -17,7 +17,7 @@
 //    lanes of a store phase hit 8 different bank groups). The accumulator's
 //    columns come out in that order; a Hadamard transform commutes with such
 //    a permutation of index bits, so the final rotation is done in it;
-//  * one thread per row tile issues tcgen05.mma: S = (Q_hi + Q_lo) K^T into
+//  * one warp per row tile issues tcgen05.mma: S = (Q_hi + Q_lo) K^T into
 //    tensor memory, and O += (P_hi + P_lo) V with P read from tensor memory;
 //  * 4 warps per row tile, one row per thread: scores from tensor memory,
 //    times the key norm, running maximum, weights times value norms as fp16
@@ -107,6 +107,24 @@ TQ_DEV uint32_t tw_levels2(uint32_t x, uint32_t lo, uint32_t hi) {
   return __byte_perm(lo, hi, (x & 0x0303u) * 0x22u + 0x1010u);
 }
 
+// Bounded wait for phase `parity` of a barrier. Twenty warps polling as
+// mbar_wait_bounded does (a clock read and a 64-bit comparison each time) took
+// half of the SM's issue slots, so this one counts its tries, and with NS > 0
+// sleeps between them (roles that run ahead of the others). False after
+// `tries` of them (a second or more).
+constexpr uint32_t TW_TRIES = 30000000u;
+constexpr int TW_NAP = 64;
+template <int NS = 0>
+TQ_DEV bool tw_wait(uint32_t bar, uint32_t parity, uint32_t tries) {
+  if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (uint32_t n = 0; n < tries; ++n) {
+    if (NS > 0) __nanosleep(NS);
+    if (mbar_try_wait(bar, parity)) return true;
+  }
+  return false;
+}
+
 TQ_DEV float tw_max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -165,7 +183,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
   constexpr int MT = C::MT, NBUF = C::NBUF;
   constexpr int PK = D * KB / 8, PV = D * VB / 8;
   extern __shared__ uint8_t raw_smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int b = blockIdx.z;
   const int split = blockIdx.x / a.hkv, hk = blockIdx.x - split * a.hkv;
   const AwSeq sq = aw_sequence(a, b, blockIdx.x == 0 && blockIdx.y == 0 && tid == 0);
@@ -238,7 +256,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::SLOT);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(sm + C::SLOT), 0);
   // row tile t: scores / weights at columns 256 t + {0, 64}, accumulator at 256 t + 128
   constexpr uint32_t FULL = 0xffffffffu;
 
@@ -248,7 +266,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
     const int w4 = (warp - C::SM_WARPS) & 3;
     // the query rows must have been read before operands take their place
     bool ok = true;
-    for (int t = 0; t < MT; ++t) ok = ok && mbar_wait_bounded(q_full + 8 * t, 0, a.wait_limit);
+    for (int t = 0; t < MT; ++t) ok = ok && tw_wait<TW_NAP>(q_full + 8 * t, 0, TW_TRIES);
     ok = __all_sync(FULL, ok);
     if (!ok && lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
     auto entry = [&](int i, int q) {  // table entry of block q of tile i
@@ -275,7 +293,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
       }
       for (int i = 0; i < cnt && ok; ++i) {
         const int buf = i % NBUF;
-        if (i >= NBUF) ok = __all_sync(FULL, mbar_wait_bounded(k_empty + 8 * buf, ((i / NBUF) - 1) & 1, a.wait_limit));
+        if (i >= NBUF) ok = __all_sync(FULL, tw_wait<TW_NAP>(k_empty + 8 * buf, ((i / NBUF) - 1) & 1, TW_TRIES));
         if (!ok) {
           if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
           break;
@@ -339,7 +357,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
       }
       for (int i = 0; i < cnt && ok; ++i) {
         const int buf = i % NBUF;
-        if (i >= NBUF) ok = __all_sync(FULL, mbar_wait_bounded(v_empty + 8 * buf, ((i / NBUF) - 1) & 1, a.wait_limit));
+        if (i >= NBUF) ok = __all_sync(FULL, tw_wait<TW_NAP>(v_empty + 8 * buf, ((i / NBUF) - 1) & 1, TW_TRIES));
         if (!ok) {
           if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
           break;
@@ -387,49 +405,63 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
     // ---- MMA issuer of row tile t
     regs_down<C::R_MMA>();
     const int t = warp - MMA_WARP;
-    if (t < MT && lane == 0) {
+    if (t < MT) {
       constexpr uint32_t ID_S = umma_idesc_f16(128, TW_TP), ID_O = umma_idesc_f16(128, D);
       const uint32_t s0 = tmem + 256u * t, o0 = s0 + 128u;
       const uint64_t q_desc = umma_desc_sw128(base + C::Q0 + 2 * t * C::Q_PART);
       const uint64_t k_desc = umma_desc_sw128(base + C::K0), v_desc = umma_desc_sw128(base + C::V0);
-      bool ok = mbar_wait_bounded(q_full + 8 * t, 0, a.wait_limit);
+      const bool active = r0 + 128 * t < rows;  // a row tile without rows only signals
+      // the whole warp waits, one elected lane issues
+      bool ok = __all_sync(FULL, tw_wait(q_full + 8 * t, 0, TW_TRIES));
       for (int i = 0; i <= cnt && ok; ++i) {
         if (i < cnt) {
           const int buf = i % NBUF;
-          ok = mbar_wait_bounded(k_full + 8 * buf, (i / NBUF) & 1, a.wait_limit);
+          ok = __all_sync(FULL, tw_wait(k_full + 8 * buf, (i / NBUF) & 1, TW_TRIES));
           if (!ok) break;
           tc_fence_after();
           const uint32_t s = s0 + 64u * (i & 1);
+          if (elect_one()) {
+            if (active) {
+              const uint64_t kd = k_desc + ((uint32_t)(buf * C::KV) >> 4);
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
+              for (int part = 0; part < 2; ++part)
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              umma_f16(s, q_desc + ((part * C::Q_PART + (ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
-                       k_desc + ((buf * C::KV + (ks >> 2) * (TW_TP * 128) + (ks & 3) * 32) >> 4), ID_S,
-                       part + ks > 0);
-          umma_commit(s_full + 16 * t + 8 * (i & 1));
-          umma_commit(k_empty + 8 * buf);
+                for (int ks = 0; ks < D / 16; ++ks)
+                  umma_f16(s, q_desc + ((part * C::Q_PART + (ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                           kd + (((ks >> 2) * (TW_TP * 128) + (ks & 3) * 32) >> 4), ID_S, part + ks > 0);
+            }
+            umma_commit(s_full + 16 * t + 8 * (i & 1));
+            umma_commit(k_empty + 8 * buf);
+          }
+          __syncwarp();
         }
         if (i > 0) {
           const int u = i - 1, buf = u % NBUF;
-          ok = mbar_wait_bounded(v_full + 8 * buf, (u / NBUF) & 1, a.wait_limit) &&
-               mbar_wait_bounded(p_full + 16 * t + 8 * (u & 1), (u >> 1) & 1, a.wait_limit);
+          ok = __all_sync(FULL, tw_wait(v_full + 8 * buf, (u / NBUF) & 1, TW_TRIES) &&
+                                    tw_wait(p_full + 16 * t + 8 * (u & 1), (u >> 1) & 1, TW_TRIES));
           if (!ok) break;
           tc_fence_after();
           const uint32_t p = s0 + 64u * (u & 1);
+          if (elect_one()) {
+            if (active) {
+              const uint64_t vd = v_desc + ((uint32_t)(buf * C::KV) >> 4);
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
+              for (int part = 0; part < 2; ++part)
 #pragma unroll
-            for (int ks = 0; ks < TW_TP / 16; ++ks)
-              umma_f16_ts(o0, p + (uint32_t)(32 * part + 8 * ks), v_desc + ((buf * C::KV + ks * 32) >> 4), ID_O,
-                          part + ks > 0 || u > 0);
-          umma_commit(o_done + 16 * t + 8 * (u & 1));
-          umma_commit(v_empty + 8 * buf);
+                for (int ks = 0; ks < TW_TP / 16; ++ks)
+                  umma_f16_ts(o0, p + (uint32_t)(32 * part + 8 * ks), vd + ((ks * 32) >> 4), ID_O,
+                              part + ks > 0 || u > 0);
+            }
+            umma_commit(o_done + 16 * t + 8 * (u & 1));
+            umma_commit(v_empty + 8 * buf);
+          }
+          __syncwarp();
         }
       }
-      if (!ok) record_error(a.err, TQ_DEVERR_TIMEOUT);
-      umma_commit(mma_end + 8 * t);
-      if (!mbar_wait_bounded(mma_end + 8 * t, 0, a.wait_limit)) record_error(a.err, TQ_DEVERR_TIMEOUT);
+      if (!ok && lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
+      if (elect_one()) umma_commit(mma_end + 8 * t);
+      __syncwarp();
+      if (!tw_wait(mma_end + 8 * t, 0, TW_TRIES) && lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
     } else if (t == 2) {
       // ---- norms and positions of the tiles, two positions per lane. A slot is
       // free again when the product two tiles back has read its keys (its
@@ -459,7 +491,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
       float v_most = 0.f, v_up = 1.f, v_inv = 1.f;
       for (int i = 0; i < cnt; ++i) {
         const int buf = i % NBUF;
-        if (i >= NBUF && !__all_sync(FULL, mbar_wait_bounded(k_empty + 8 * buf, ((i / NBUF) - 1) & 1, a.wait_limit))) {
+        if (i >= NBUF && !__all_sync(FULL, tw_wait<TW_NAP>(k_empty + 8 * buf, ((i / NBUF) - 1) & 1, TW_TRIES))) {
           if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
           break;
         }
@@ -592,8 +624,8 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
     float m_ref = -INFINITY, l_sum = 0.f, v_inv = 1.f;
     bool ok = true;
     for (int i = 0; i < cnt; ++i) {
-      ok = mbar_wait_bounded(s_full + 16 * mt + 8 * (i & 1), (i >> 1) & 1, a.wait_limit) &&
-           mbar_wait_bounded(n_full + 8 * (i % TW_SLOTS), (i / TW_SLOTS) & 1, a.wait_limit);
+      ok = tw_wait(s_full + 16 * mt + 8 * (i & 1), (i >> 1) & 1, TW_TRIES) &&
+           tw_wait(n_full + 8 * (i % TW_SLOTS), (i / TW_SLOTS) & 1, TW_TRIES);
       ok = __all_sync(FULL, ok);
       if (!ok) {
         if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
@@ -661,7 +693,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
           // may be the first in many tiles, and this one's earlier phases
           // ended before the scores of tile i - 1 were complete.)
           const bool done = __all_sync(
-              FULL, mbar_wait_bounded(o_done + 16 * mt + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, a.wait_limit));
+              FULL, tw_wait(o_done + 16 * mt + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, TW_TRIES));
           if (!done) {
             if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
             ok = false;
@@ -691,7 +723,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
     }
     // ---- results
     if (ok && cnt > 0) {
-      ok = __all_sync(FULL, mbar_wait_bounded(mma_end + 8 * mt, 0, a.wait_limit));  // every product is done
+      ok = __all_sync(FULL, tw_wait(mma_end + 8 * mt, 0, TW_TRIES));  // every product is done
       if (!ok && lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
       tc_fence_after();
     }

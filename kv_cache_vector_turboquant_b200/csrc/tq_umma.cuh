@@ -60,6 +60,20 @@ TQ_DEV void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
 TQ_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 TQ_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// One lane of a converged warp (always the same one). Code under this branch
+// is known to run in one thread, so what it issues takes its descriptors from
+// uniform registers; under `lane == 0` each tcgen05.mma went through a loop
+// over the lanes (100 cycles and more of the issuing warp).
+TQ_DEV bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+
 // ---------------------------------------------------------------- MMA
 // D[tmem] (+)= A[adesc] * B[bdesc]^T, issued by a single thread.
 TQ_DEV void umma_f16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool accumulate) {

@@ -235,15 +235,17 @@ def test_offsets_and_lengths_out_of_range_are_flagged(K):
     good = torch.tensor([0, 2, 4, 6], dtype=torch.int32, device="cuda")
     ref = K.attend_window(q, kc, vc, kp, kn, vp, vn, ctx, q_offsets=good, max_q=2)
     assert K.tq_device_error() == (K.TQ_OK, 0)
-    # decreasing, past the tokens, negative, more than max_q: those sequences are left out
-    for off, kept in (([0, 2, 1, 3], [0]), ([0, 2, 4, 7], [0, 1]), ([-1, 2, 4, 6], [1, 2]), ([0, 2, 6, 6], [0])):
+    # decreasing, past the tokens, negative, more than max_q: those sequences
+    # are left out. (The first: [0, 2), none, [1, 3): tokens 1 and 2 belong to
+    # the last sequence too, so token 0 alone has one value.)
+    for off, kept in (([0, 2, 1, 3], [0]), ([0, 2, 4, 7], [0, 1, 2, 3]), ([-1, 2, 4, 6], [2, 3, 4, 5]),
+                      ([0, 2, 6, 6], [0, 1])):
         out = torch.full_like(q, 7.0)
         K.attend_window(q, kc, vc, kp, kn, vp, vn, ctx, q_offsets=torch.tensor(off, dtype=torch.int32, device="cuda"),
                         max_q=2, out=out)
         torch.cuda.synchronize()
         assert K.tq_device_error() == (K.TQ_ERR_DEVICE, K.TQ_DEVERR_ROW_RANGE)
-        for b in kept:
-            assert torch.equal(out[2 * b:2 * b + 2], ref[2 * b:2 * b + 2])
+        assert torch.equal(out[kept], ref[kept])
     long = torch.tensor([99, 32, 32], dtype=torch.int32, device="cuda")  # clamped to the cache
     got = K.attend_window(q, kc, vc, kp, kn, vp, vn, long, q_offsets=good, max_q=2)
     assert torch.equal(got, ref)
