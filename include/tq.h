@@ -397,7 +397,8 @@ size_t tq_attend_window_workspace_bytes(int64_t n_tok, int B, int max_q, int hq,
  *   out_f16     device, [n_tok, hq, d] fp16 out, 16-byte aligned.
  *   workspace   at least tq_attend_window_workspace_bytes(...) bytes, 16-byte
  *               aligned (NULL if that is 0); contents on entry do not matter.
- * Any hq that is a multiple of hkv. s_max below 2^31 - 256, B at most 65535.
+ * Any hq that is a multiple of hkv; hkv at most 65536, s_max below 2^31 - 256,
+ * B at most 65535.
  * Asynchronous on `stream`; calls that share a workspace must not overlap.
  */
 tq_status tq_attend_window(const tq_ctx* k, const tq_ctx* v, const void* q_f16, int64_t n_tok, int B,

@@ -486,6 +486,25 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
     return f.to(device), scale
 
 
+def _span(t):
+    """First address of a tensor and the first behind it."""
+    n = sum((k - 1) * s for k, s in zip(t.shape, t.stride())) + 1 if t.numel() else 0
+    return t.data_ptr(), t.data_ptr() + n * t.element_size()
+
+
+def _apart(name, out, others, itself=None):
+    """Refuse an output that shares memory with `others` (and with `itself`,
+    unless it is that very tensor)."""
+    lo, hi = _span(out)
+    if itself is not None and not (itself.data_ptr() == lo and itself.stride() == out.stride()
+                                   and itself.dtype is out.dtype):
+        others = (*others, itself)
+    for t in others:
+        a, b = _span(t)
+        if lo < b and a < hi:
+            raise ValueError(f"{name}: shares memory with another argument")
+
+
 def _head_rows(t, name):
     """Strides of a [T, H, d] view whose rows are dense and 16-byte aligned."""
     s0, s1, s2 = t.stride()
@@ -505,7 +524,7 @@ def qk_norm_rope(q, k, positions, inv_freq=None, *, interleaved: bool = False, r
     in q's dtype or float32, None for no norm of that tensor. Returns (q, k)
     fp16 [T, H, d]: keys as `encode_slots` takes them, queries as the attention
     calls do. `out` = (q_out, k_out), which may be q and k where they are
-    contiguous fp16.
+    contiguous fp16, and share no memory with the inputs otherwise.
     """
     import torch
 
@@ -547,6 +566,8 @@ def qk_norm_rope(q, k, positions, inv_freq=None, *, interleaved: bool = False, r
     if out is not None:
         _check(qo, "out q", half, shape=(T, hq, d))
         _check(ko, "out k", half, shape=(T, hkv, d))
+        _apart("out q", qo, (k, ko), q)
+        _apart("out k", ko, (q, qo), k)
     dev = _one_device(("q", "k", "positions", "inv_freq", "q_weight", "k_weight", "out q", "out k"),
                       (q, k, positions, inv_freq, q_weight, k_weight, qo, ko))
     if _elsewhere(dev, stream):
@@ -692,6 +713,17 @@ def _page_state(block_tables, context_lens, refs, num_blocks):
     return rows, max_blocks
 
 
+def _page_outputs(out, inputs, lists=(), more=()):
+    """Checks of page outputs: like the inputs, each of them its own input or
+    apart from everything else (`lists`: inputs without an output, `more`:
+    outputs without an input, whose sizes have been checked)."""
+    for i, (o, t) in enumerate(zip(out, inputs)):
+        _check(o, "out", t.dtype, shape=t.shape)
+        _apart("out", o, (*inputs[:i], *inputs[i + 1:], *out[:i], *out[i + 1:], *lists, *more), t)
+    for i, o in enumerate(more):
+        _apart("out", o, (*inputs, *lists, *more[:i], *more[i + 1:]))
+
+
 def pages_trim(block_tables, context_lens, refs, window=None, sinks: int = 0, release=None, out=None, stream=None):
     """Give pages back: all pages of rows with release[row] true (their length
     becomes 0), and of the others those that no query of `attend_window_paged`
@@ -712,8 +744,7 @@ def pages_trim(block_tables, context_lens, refs, window=None, sinks: int = 0, re
     if release is not None:
         _check(release, "release", torch.bool if release.dtype is torch.bool else (torch.bool, torch.uint8), numel=rows)
     if out is not None:
-        _page_state(*out, refs.numel())
-        _require(out[0].shape == block_tables.shape, "out: tables of the same shape")
+        _page_outputs(out, (block_tables, context_lens, refs))
     dev = _one_device(("block_tables", "context_lens", "refs", "release", "out", "out", "out"),
                       (block_tables, context_lens, refs, release, *(out if out is not None else ())))
     if _elsewhere(dev, stream):
@@ -774,8 +805,7 @@ class TQPagePools:
         if not n <= rows <= TQ_MAX_PAGE_ROWS:
             raise ValueError(f"at most {rows} forks of at most {TQ_MAX_PAGE_ROWS} rows")
         if out is not None:
-            _page_state(*out, self.num_blocks)
-            _require(out[0].shape == block_tables.shape, "out: tables of the same shape")
+            _page_outputs(out, (block_tables, context_lens, refs), (parents, children))
         if workspace is not None:
             _check(workspace, "workspace", torch.uint8)
         self._on_mine(("block_tables", "context_lens", "refs", "parents", "children", "workspace", "out", "out", "out"),
@@ -804,10 +834,9 @@ class TQPagePools:
         if rows > TQ_MAX_PAGE_ROWS:
             raise ValueError(f"block_tables: at most {TQ_MAX_PAGE_ROWS} rows")
         if out is not None:
-            _page_state(out[0], None, out[1], self.num_blocks)
-            _require(out[0].shape == block_tables.shape, "out: tables of the same shape")
             _check(out[2], "out remap", torch.int32, numel=self.num_blocks)
             _check(out[3], "out used", torch.int32, numel=1)
+            _page_outputs(out[:2], (block_tables, refs), (), out[2:])
         if workspace is not None:
             _check(workspace, "workspace", torch.uint8)
         self._on_mine(("block_tables", "refs", "workspace", "out", "out", "out", "out"),

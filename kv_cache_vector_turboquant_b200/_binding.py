@@ -11,6 +11,7 @@ raises ``ImportError`` if the library has not been built
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtq.so")
@@ -288,12 +289,13 @@ def tq_qk_norm_rope(q, k, dtype: int, n_tok: int, hq: int, hkv: int, head_dim: i
                     q_head_stride: int, k_tok_stride: int, k_head_stride: int, positions, inv_freq, rot_dim: int,
                     interleaved: bool, rope_scale: float, q_weight, k_weight, weight_f32: bool, eps: float, q_out,
                     k_out, stream=None) -> None:
-    _check(_lib.tq_qk_norm_rope(_ptr(q), _ptr(k), dtype, n_tok, hq, hkv, head_dim, q_tok_stride, q_head_stride,
-                                k_tok_stride, k_head_stride, _ptr(positions), _ptr(inv_freq), rot_dim,
+    _check(_lib.tq_qk_norm_rope(q.data_ptr(), k.data_ptr(), dtype, n_tok, hq, hkv, head_dim, q_tok_stride, q_head_stride,
+                                k_tok_stride, k_head_stride, positions.data_ptr(), _ptr(inv_freq), rot_dim,
                                 int(interleaved), rope_scale, _ptr(q_weight), _ptr(k_weight), int(weight_f32), eps,
-                                _ptr(q_out), _ptr(k_out), _stream(stream)), "tq_qk_norm_rope")
+                                q_out.data_ptr(), k_out.data_ptr(), _stream(stream)), "tq_qk_norm_rope")
 
 
+@functools.lru_cache(maxsize=256)  # a function of the sizes alone; a decode loop asks for the same ones
 def tq_attend_window_workspace_bytes(n_tok: int, B: int, max_q: int, hq: int, hkv: int, head_dim: int, s_max: int,
                                      window: int, sinks: int) -> int:
     return _lib.tq_attend_window_workspace_bytes(n_tok, B, max_q, hq, hkv, head_dim, s_max, window, sinks)
@@ -302,18 +304,18 @@ def tq_attend_window_workspace_bytes(n_tok: int, B: int, max_q: int, hq: int, hk
 def tq_attend_window(k: Ctx, v: Ctx, q, n_tok: int, B: int, q_offsets, max_q: int, hq: int, hkv: int, k_cache,
                      k_norms, v_cache, v_norms, s_max: int, context_lens, window: int, sinks: int, out, workspace,
                      ws_bytes: int, stream=None) -> None:
-    _check(_lib.tq_attend_window(k.handle, v.handle, _ptr(q), n_tok, B, _ptr(q_offsets), max_q, hq, hkv,
-                                 _ptr(k_cache), _ptr(k_norms), _ptr(v_cache), _ptr(v_norms), s_max,
-                                 _ptr(context_lens), window, sinks, _ptr(out), _ptr(workspace), ws_bytes,
+    _check(_lib.tq_attend_window(k.handle, v.handle, q.data_ptr(), n_tok, B, _ptr(q_offsets), max_q, hq, hkv,
+                                 k_cache.data_ptr(), k_norms.data_ptr(), v_cache.data_ptr(), v_norms.data_ptr(), s_max,
+                                 context_lens.data_ptr(), window, sinks, out.data_ptr(), _ptr(workspace), ws_bytes,
                                  _stream(stream)), "tq_attend_window")
 
 
 def tq_attend_window_paged(k: Ctx, v: Ctx, q, n_tok: int, B: int, q_offsets, max_q: int, hq: int, hkv: int, k_cache,
                            k_norms, v_cache, v_norms, num_blocks: int, block_tables, max_blocks: int, context_lens,
                            window: int, sinks: int, out, workspace, ws_bytes: int, stream=None) -> None:
-    _check(_lib.tq_attend_window_paged(k.handle, v.handle, _ptr(q), n_tok, B, _ptr(q_offsets), max_q, hq, hkv,
-                                       _ptr(k_cache), _ptr(k_norms), _ptr(v_cache), _ptr(v_norms), num_blocks,
-                                       _ptr(block_tables), max_blocks, _ptr(context_lens), window, sinks, _ptr(out),
+    _check(_lib.tq_attend_window_paged(k.handle, v.handle, q.data_ptr(), n_tok, B, _ptr(q_offsets), max_q, hq, hkv,
+                                       k_cache.data_ptr(), k_norms.data_ptr(), v_cache.data_ptr(), v_norms.data_ptr(), num_blocks,
+                                       block_tables.data_ptr(), max_blocks, context_lens.data_ptr(), window, sinks, out.data_ptr(),
                                        _ptr(workspace), ws_bytes, _stream(stream)), "tq_attend_window_paged")
 
 
@@ -325,15 +327,15 @@ def tq_pages_fork(pools, n_pools: int, num_blocks: int, block_tables, tables_out
                   n_rows: int, max_blocks: int, parents, children, n: int, workspace, ws_bytes: int,
                   stream=None) -> None:
     """`pools`: a ctypes array of PagePool."""
-    _check(_lib.tq_pages_fork(pools, n_pools, num_blocks, _ptr(block_tables), _ptr(tables_out), _ptr(lens),
-                              _ptr(lens_out), _ptr(refs), _ptr(refs_out), n_rows, max_blocks, _ptr(parents),
-                              _ptr(children), n, _ptr(workspace), ws_bytes, _stream(stream)), "tq_pages_fork")
+    _check(_lib.tq_pages_fork(pools, n_pools, num_blocks, block_tables.data_ptr(), tables_out.data_ptr(), lens.data_ptr(),
+                              lens_out.data_ptr(), refs.data_ptr(), refs_out.data_ptr(), n_rows, max_blocks, parents.data_ptr(),
+                              children.data_ptr(), n, _ptr(workspace), ws_bytes, _stream(stream)), "tq_pages_fork")
 
 
 def tq_pages_trim(block_tables, tables_out, lens, lens_out, refs, refs_out, n_rows: int, max_blocks: int,
                   num_blocks: int, window: int, sinks: int, release, stream=None) -> None:
-    _check(_lib.tq_pages_trim(_ptr(block_tables), _ptr(tables_out), _ptr(lens), _ptr(lens_out), _ptr(refs),
-                              _ptr(refs_out), n_rows, max_blocks, num_blocks, window, sinks, _ptr(release),
+    _check(_lib.tq_pages_trim(block_tables.data_ptr(), tables_out.data_ptr(), lens.data_ptr(), lens_out.data_ptr(), refs.data_ptr(),
+                              refs_out.data_ptr(), n_rows, max_blocks, num_blocks, window, sinks, _ptr(release),
                               _stream(stream)), "tq_pages_trim")
 
 
@@ -344,8 +346,8 @@ def tq_pages_compact_workspace_bytes(num_blocks: int) -> int:
 def tq_pages_compact(pools, n_pools: int, num_blocks: int, block_tables, tables_out, refs, refs_out, n_rows: int,
                      max_blocks: int, remap, used, workspace, ws_bytes: int, stream=None) -> None:
     """`pools`: a ctypes array of PagePool."""
-    _check(_lib.tq_pages_compact(pools, n_pools, num_blocks, _ptr(block_tables), _ptr(tables_out), _ptr(refs),
-                                 _ptr(refs_out), n_rows, max_blocks, _ptr(remap), _ptr(used), _ptr(workspace),
+    _check(_lib.tq_pages_compact(pools, n_pools, num_blocks, block_tables.data_ptr(), tables_out.data_ptr(), refs.data_ptr(),
+                                 refs_out.data_ptr(), n_rows, max_blocks, remap.data_ptr(), used.data_ptr(), _ptr(workspace),
                                  ws_bytes, _stream(stream)), "tq_pages_compact")
 
 

@@ -746,8 +746,8 @@ static int window_splits(int B, int hq, int hkv, int max_q, int d, int64_t s_max
 template <int D, int KB, int VB, int NT>
 static cudaError_t launch_window_t(const AwArgs& a, cudaStream_t st) {
   using C = AwCfg<D, KB, VB, NT>;
-  cudaError_t e = cudaFuncSetAttribute(window_partial_kernel<D, KB, VB, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, AW_SMEM);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = aw_allow_smem(reinterpret_cast<const void*>(window_partial_kernel<D, KB, VB, NT>), AW_SMEM, done);
   if (e != cudaSuccess) return e;
   const int64_t gx = ((int64_t)a.n_split * a.hkv + C::WARPS - 1) / C::WARPS;
   const int64_t gy = ((int64_t)a.max_q * a.g + 4 * NT - 1) / (4 * NT);

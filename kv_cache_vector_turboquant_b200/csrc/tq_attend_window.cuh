@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "tq_attend.cuh"
 
@@ -173,6 +174,19 @@ TQ_DEV uint32_t aw_bits(const uint32_t (&w)[N], int off) {
   uint32_t f = w[off >> 5] >> (off & 31);
   if ((off & 31) + NB > 32 && (off >> 5) + 1 < N) f |= w[(off >> 5) + 1] << (32 - (off & 31));
   return f & ((1u << NB) - 1u);
+}
+
+// Let `kernel` use `bytes` of dynamic shared memory, once per device (`done`:
+// a bit per device, one word per kernel instance).
+inline cudaError_t aw_allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace tq

@@ -798,8 +798,8 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
 template <int D, int KB, int VB>
 static cudaError_t launch_tc_t(const AwArgs& a, cudaStream_t st) {
   using C = TwCfg<D, KB, VB>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(window_tc_kernel<D, KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = aw_allow_smem(reinterpret_cast<const void*>(window_tc_kernel<D, KB, VB>), C::BYTES, done);
   if (e != cudaSuccess) return e;
   const int64_t gx = (int64_t)a.n_split * a.hkv, gy = ((int64_t)a.max_q * a.g + 128 * C::MT - 1) / (128 * C::MT);
   if (gx > 0x7fffffff || gy > 65535) return cudaErrorNotSupported;

@@ -421,7 +421,7 @@ static tq_status attend_window(const tq_ctx* k, const tq_ctx* v, const void* q_f
   if (n_tok < 0 || B < 0 || max_q <= 0 || hq <= 0 || hkv <= 0 || hq % hkv != 0 || s_max <= 0 || sinks < 0)
     return TQ_ERR_INVALID_ARG;
   if (!q_offsets && (max_q != 1 || n_tok != B)) return TQ_ERR_INVALID_ARG;
-  if (B > 65535 || s_max >= ((int64_t)1 << 31) - 256) return TQ_ERR_UNSUPPORTED;
+  if (B > 65535 || hkv > 65536 || s_max >= ((int64_t)1 << 31) - 256) return TQ_ERR_UNSUPPORTED;
   if (n_tok > 0x7fffffff || (int64_t)max_q * (hq / hkv) > 0x3fffffff) return TQ_ERR_UNSUPPORTED;
   if (B == 0 || n_tok == 0) return TQ_OK;
   if (!q_f16 || !k_cache || !k_norms || !v_cache || !v_norms || !context_lens || !out_f16) return TQ_ERR_INVALID_ARG;

@@ -503,11 +503,13 @@ tq_status tq_launch_pages_fork(const tq_page_pool* pools, int n_pools, int64_t n
   const int sms = tq_sm_count(dev);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool copies = tables_out != tables || lens_out != lens || refs_out != refs;
+  if (n == 0 && !copies) return TQ_OK;
   const int64_t ints = (int64_t)n_rows * max_blocks + num_blocks;
   const int plan_grid = 1 + (copies ? (int)std::min<int64_t>(sms, ints / PG_SEG + 1) : 0);
   const size_t smem = (size_t)((n_rows + 31) / 32) * 12;
   fork_plan_kernel<<<plan_grid, PG_PLAN_THREADS, smem, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
+  if (n == 0) return TQ_OK;
   const PgPools p = make_pools(pools, n_pools);
   const int64_t warps = (int64_t)p.unit0[n_pools] * n;
   const int grid = (int)std::min<int64_t>(6 * sms, std::max<int64_t>(n, (warps + 7) / 8));

@@ -91,6 +91,18 @@ def test_fork(K, rows, mb, nb, live, n, layers, hkv, pk, pv, inplace):
     assert K.tq_device_error()[1] == (K.TQ_DEVERR_POOL_FULL if full else 0)
 
 
+def test_no_forks(K):
+    """An empty list copies the tables, or does nothing in place."""
+    rng = random.Random(5)
+    t, l, r = (_i32(x) for x in _state(rng, 5, 3, 20, 3))
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    h = K.TQPagePools(_pools(20, 1, 1, 16, 16, 1))
+    for out in (None, (t, l, r)):
+        got = h.fork(t, l, r, none, none, out=out)
+        assert all(torch.equal(a, b) for a, b in zip(got, (t, l, r)))
+    assert K.tq_device_error() == (K.TQ_OK, 0)
+
+
 def test_fork_skips_and_flags_impossible_pairs(K):
     rng = random.Random(5)
     table, lens, refs = _state(rng, 12, 4, 40, 6)

@@ -169,6 +169,46 @@ def test_empty_contexts_and_unseen_tokens(K):
     assert torch.all(one == 0)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_rows_with_empty_and_short_contexts(K, d):
+    """The same for sequences of many query tokens (one more than a row tile of
+    some, an empty one between, more tokens than positions), with a replaced
+    offset row behind them left alone."""
+    S, hq, hkv, kb, vb = 150, 2, 2, 4, 3
+    n, lens = [129, 0, 60, 45, 41], [150, 7, 13, 0, 41]
+    B = len(n)
+    kc, kp, kn = _cache(K, (B, S, hkv), d, kb, 1)
+    vc, vp, vn = _cache(K, (B, S, hkv), d, vb, 2)
+    off = np.concatenate([[0], np.cumsum(n)])
+    q = (0.5 * torch.randn(int(off[-1]) + 3, hq, d, device="cuda")).half()
+    out = torch.full_like(q, 7.0)
+    K.attend_window(q, kc, vc, kp, kn, vp, vn, torch.tensor(lens, dtype=torch.int32, device="cuda"), window=20, sinks=3,
+                    q_offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), max_q=129, out=out)
+    torch.cuda.synchronize()
+    assert K.tq_device_error() == (K.TQ_OK, 0)
+    assert torch.all(out[off[-1]:] == 7.0)
+    for b in range(B):
+        if not n[b]:
+            continue
+        kk, vv = R.decode_rows(kp[b], kn[b], kb, d), R.decode_rows(vp[b], vn[b], vb, d)
+        ref, tol = R.attend(q[off[b]:off[b + 1]], kk, vv, lens[b], 20, 3, kb, vb)
+        _check(out[off[b]:off[b + 1]], ref, tol)
+    assert torch.all(out[off[2]:off[2] + 47] == 0) and torch.all(out[off[3]:off[4]] == 0)
+
+
+@pytest.mark.parametrize("n", [1, 48])
+def test_output_in_place_of_the_queries(K, n):
+    d, S, hq, hkv = 128, 700, 8, 2
+    kc, kp, kn = _cache(K, (1, S, hkv), d, 4, 1)
+    vc, vp, vn = _cache(K, (1, S, hkv), d, 4, 2)
+    q = torch.randn(n, hq, d, device="cuda").half()
+    args = (kc, vc, kp, kn, vp, vn, torch.tensor([S], dtype=torch.int32, device="cuda"), 300, 4,
+            torch.tensor([0, n], dtype=torch.int32, device="cuda"), n)
+    ref = K.attend_window(q, *args)
+    K.attend_window(q, *args, out=q)
+    assert torch.equal(q, ref)
+
+
 def test_non_finite_norms_where_no_query_looks(K):
     """Norms of NaN and infinity behind the context, outside the window and in
     unread pages leave the results as they are."""

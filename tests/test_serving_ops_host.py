@@ -43,6 +43,13 @@ def test_norm_rope_refusals(K):
     _raises(lambda: f_(q, k, pos, f, eps=float("nan")), "eps")
     _raises(lambda: f_(q, k, pos, f, out=(q, k.float())), "out k: dtype")
     _raises(lambda: f_(q, k, pos, f, out=(q[:4], k)), "out q: shape")
+    same = k.clone()
+    _raises(lambda: f_(k, k.clone(), pos, f, out=(same, same)), "shares memory")
+    _raises(lambda: f_(k.clone(), k, pos, f, out=(k, torch.empty_like(k))), "shares memory")
+    slab = torch.zeros(5 * 4 * 128 + 8, dtype=torch.float16)
+    _raises(lambda: f_(slab[:2560].view(5, 4, 128), k, pos, f, out=(slab[8:].view(5, 4, 128), same)), "shares memory")
+    _raises(lambda: f_(q.bfloat16(), k.bfloat16(), pos, f, out=(q, k)), "CUDA")
+    _raises(lambda: f_(q, k, pos, f, out=(q, k)), "CUDA")  # in place is fine
     wide = torch.zeros(5, 4, 132, dtype=torch.float16)[..., :128]
     _raises(lambda: f_(wide, k, pos, f), "strides")
     off = torch.zeros(5 * 4 * 128 + 1, dtype=torch.float16)[1:].view(5, 4, 128)
@@ -121,8 +128,13 @@ def test_page_refusals(K):
     _raises(lambda: f(t, n, r, window=-1), "window")
     _raises(lambda: f(t, n, r, sinks=-1), "sinks")
     _raises(lambda: f(t, n, r, release=n), "release: dtype")
-    _raises(lambda: f(t, n, r, out=(t[:2], n[:2], r)), "same shape")
-    _raises(lambda: f(t, n, r, out=(t, n, r[:5])), "refs")
+    _raises(lambda: f(t, n, r, out=(t[:2], n[:2], r)), "out: shape")
+    _raises(lambda: f(t, n, r, out=(t, n, r[:5])), "out: shape")
+    _raises(lambda: f(t, n, r, out=(t, n, r)), "CUDA")
+    both = torch.zeros(20, dtype=torch.int32)
+    _raises(lambda: f(t, n, r, out=(both[:12].view(3, 4), both[11:14], r.clone())), "shares memory")
+    _raises(lambda: f(both[:12].view(3, 4), n, r, out=(both[1:13].view(3, 4), n, r)), "shares memory")
+    _raises(lambda: f(t, n, r, out=(t.clone(), t[0, :3], r)), "shares memory")
     P = K.TQPagePools
     pool = torch.zeros(9, 16, 2, 16, dtype=torch.uint8)
     _raises(lambda: P([]), "pools")
@@ -158,7 +170,7 @@ def test_abi_refusals(K):
     assert aw(T=0, B=0, q=None) == K.TQ_OK and aw(T=0, off=p, q=None) == K.TQ_OK
     assert aw(k=None) == aw(v=small) == aw(hq=3) == aw(hkv=0) == aw(S=0) == aw(sinks=-1) == K.TQ_ERR_INVALID_ARG
     assert aw(T=3) == aw(mq=2) == aw(mq=0) == aw(q=None) == aw(ctx=None) == aw(T=-1) == K.TQ_ERR_INVALID_ARG
-    assert aw(S=1 << 31) == aw(T=65536, B=65536) == K.TQ_ERR_UNSUPPORTED
+    assert aw(S=1 << 31) == aw(T=65536, B=65536) == aw(hq=1 << 17, hkv=1 << 17) == K.TQ_ERR_UNSUPPORTED
     assert aw(q=p + 2) == aw(ctx=p + 2) == aw(off=p + 2, mq=2) == aw(ws=p + 4) == K.TQ_ERR_ALIGNMENT
     assert aw(ws=None) == aw(wsn=16) == K.TQ_ERR_WORKSPACE
     ws = K.tq_attend_window_workspace_bytes
