@@ -52,8 +52,8 @@ struct TwSlot {
   int t_min, t_max;  // first and last position
   float v_fix;       // this tile's power of two over the previous tile's
   float v_inv;       // its inverse
-  int odd;           // some norm is infinite or NaN
-  int pad[3];
+  uint32_t odd[2];   // positions whose value norm is infinite or NaN (0 in nv)
+  int pad[2];
 };
 
 template <int D, int KB, int VB>
@@ -133,8 +133,7 @@ TQ_DEV float tw_max3(float a, float b, float c) {
 
 // Weights 2^(x row_inv - ref) of a row's 64 scores; returns their sum and
 // stores weight x value norm as fp16 value (columns 0-31 from `col`) and
-// remainder (32-63).
-template <bool CHECK>
+// remainder (32-63). (A masked score's weight is 0 times a finite norm.)
 TQ_DEV float tw_weights(const float (&x)[64], const float* nv, float row_inv, float ref, uint32_t col) {
   f2 sum = make_float2(0.f, 0.f);
   const f2 scale = make_float2(row_inv, row_inv), shift = make_float2(-ref, -ref);
@@ -150,11 +149,7 @@ TQ_DEV float tw_weights(const float (&x)[64], const float* nv, float row_inv, fl
         const f2 z = fma2(make_float2(x[e], x[e + 1]), scale, shift);
         const f2 p = make_float2(aw_exp2(z.x), aw_exp2(z.y));
         sum = add2(sum, p);
-        f2 w = mul2(p, k ? make_float2(n4.z, n4.w) : make_float2(n4.x, n4.y));
-        if (CHECK) {
-          if (x[e] == -INFINITY) w.x = 0.f;
-          if (x[e + 1] == -INFINITY) w.y = 0.f;
-        }
+        const f2 w = mul2(p, k ? make_float2(n4.z, n4.w) : make_float2(n4.x, n4.y));
         const uint32_t h2 = pack_half2(w.x, w.y);
         const f2 r = sub2(w, __half22float2(*reinterpret_cast<const __half2*>(&h2)));
         hi[c / 2 + k] = h2;
@@ -165,6 +160,13 @@ TQ_DEV float tw_weights(const float (&x)[64], const float* nv, float row_inv, fl
     tmem_st16(col + 32u + (uint32_t)(c0 / 2), lo);
   }
   return sum.x + sum.y;
+}
+
+// The visible ones (aw_visible) of the 16 positions from t0 on, as bits.
+TQ_DEV uint32_t tw_visible16(int t0, int p, int window, int sinks) {
+  const int seen = min(max(p - t0 + 1, 0), 16), before = min(max(max(p - window + 1, 0) - t0, 0), 16),
+            first = min(max(sinks - t0, 0), 16);
+  return ((1u << seen) - 1u) & (~((1u << before) - 1u) | ((1u << first) - 1u));
 }
 
 template <int N>
@@ -521,20 +523,19 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
           v_up = up;
           v_inv = inv;
         }
-        bool fine = true;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          const bool fine = fabsf(nv[h]) < INFINITY;
           s.nk[32 * h + lane] = nk[h];
-          s.nv[32 * h + lane] = nv[h] * v_up;
-          fine = fine && fabsf(nk[h]) < INFINITY && fabsf(nv[h]) < INFINITY;
+          s.nv[32 * h + lane] = fine ? nv[h] * v_up : 0.f;
+          const uint32_t odd = __ballot_sync(FULL, !fine);
+          if (lane == 0) s.odd[h] = odd;
         }
-        fine = __all_sync(FULL, fine);
         if (lane == 0) {
           s.t_min = t_min;
           s.t_max = t_max;
           s.v_fix = fix;
           s.v_inv = v_inv;
-          s.odd = !fine;
         }
         if (i + 1 < cnt) fetch(i + 1);
         mbar_arrive(n_full + 8 * (i % TW_SLOTS));
@@ -659,10 +660,10 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
         if (hidden) {
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            const int t0 = slot.blk_t[h];
+            const uint32_t seen = tw_visible16(slot.blk_t[h], p_row, a.window, a.sinks);
 #pragma unroll
             for (int c = 0; c < 16; ++c)
-              if (!aw_visible(t0 + c, p_row, a.window, a.sinks)) x[16 * h + c] = -INFINITY;
+              if (!(seen >> c & 1u)) x[16 * h + c] = -INFINITY;
           }
         }
         float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
@@ -712,10 +713,14 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
           }
         }
         const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-        // a masked position's norm may be infinite or NaN: its weight is then
-        // cleared by comparison instead of by its factor 0
-        l_sum += hidden && slot.odd ? tw_weights<true>(x, slot.nv, row_inv, ref, sp)
-                                    : tw_weights<false>(x, slot.nv, row_inv, ref, sp);
+        l_sum += tw_weights(x, slot.nv, row_inv, ref, sp);
+        if (slot.odd[0] | slot.odd[1]) {  // value norms that are infinite or NaN: NaN for the rows that see one
+#pragma unroll 1
+          for (int c = 0; c < TW_TP; ++c)
+            if ((slot.odd[c >> 5] >> (c & 31) & 1u) &&
+                aw_visible(slot.blk_t[c >> 4] + (c & 15), p_row, a.window, a.sinks))
+              l_sum = __int_as_float(0x7fc00000);
+        }
         tmem_wait_st();
       }
       tc_fence_before();

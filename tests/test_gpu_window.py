@@ -230,6 +230,30 @@ def test_non_finite_norms_where_no_query_looks(K):
     assert torch.equal(ref[1], got[1]) and torch.equal(ref[0, :4], got[0, :4]) and got[0, 4:].isnan().all()
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("n", [4, 64])
+def test_non_finite_norms_reach_the_rows_that_see_them(K, n, bad):
+    """A value norm that is not finite: NaN or infinite rows for the queries of
+    its kv head that see the position, the others as they were (few and many
+    query rows)."""
+    d, S, hq, hkv, window, sinks = 128, 300, 4, 2, 40, 2
+    kc, kp, kn = _cache(K, (1, S, hkv), d, 4, 1)
+    vc, vp, vn = _cache(K, (1, S, hkv), d, 2, 2)
+    q = torch.randn(n, hq, d, device="cuda").half()
+    args = (torch.tensor([S], dtype=torch.int32, device="cuda"), window, sinks,
+            torch.tensor([0, n], dtype=torch.int32, device="cuda"), n)
+    ref = K.attend_window(q, kc, vc, kp, kn, vp, vn, *args)
+    at = S - 42  # seen by the tokens at positions below at + 40
+    vn[0, at, 1] = bad
+    got = K.attend_window(q, kc, vc, kp, kn, vp, vn, *args)
+    p = torch.arange(S - n, S, device="cuda")
+    hit = torch.zeros(n, hq, dtype=torch.bool, device="cuda")
+    hit[(p >= at) & (p - at < window), 2:] = True
+    assert torch.equal(got[~hit], ref[~hit])
+    assert not torch.isfinite(got[hit]).any(-1).any() if hit.any() else True
+    assert hit.any() and not hit.all()
+
+
 @pytest.mark.parametrize("n,S", [(1, 40), (1, 2000), (40, 100), (40, 3000)])
 def test_a_nan_query_gives_its_own_rows_nan(K, n, S):
     """One and several splits, few and many query rows."""
