@@ -11,6 +11,9 @@ TurboQuant", "API Reference": ``TurboQuant(head_dim, bits, seed=42)``,
 from __future__ import annotations
 
 import contextlib
+import ctypes
+import functools
+import importlib
 
 from ._binding import (  # noqa: F401
     LIB_PATH,
@@ -134,19 +137,25 @@ def _one_device(names, tensors) -> int:
     return dev
 
 
-def _elsewhere(dev: int, stream) -> bool:
-    """Whether a call has to be made inside `_launching`: a stream is given, or
-    the tensors' device is not the current one."""
+@functools.cache
+def _calls():
+    """The compiled checks and calls of the operators around the cache."""
+    import torch  # noqa: F401  (the extension is linked against its libraries)
+
+    try:
+        return importlib.import_module("._ops", __name__)
+    except ImportError as e:
+        raise ImportError("_ops.so is missing or does not fit the installed torch; build it with "
+                          "`python kv_cache_vector_turboquant_b200/build.py`") from e
+
+
+def _on_stream(stream, name, t, call, *args):
+    """`call` inside `stream`, one of the device that holds the tensor `t`."""
     import torch
 
-    return stream is not None or torch.cuda.current_device() != dev
-
-
-def _raw_stream(dev: int) -> int:
-    """Handle of the current stream of the current device."""
-    import torch
-
-    return torch._C._cuda_getCurrentRawStream(dev)
+    _require(isinstance(t, torch.Tensor) and t.is_cuda, f"{name}: a CUDA tensor")
+    with _launching(t.device, stream):
+        return call(*args)
 
 
 class TurboQuant:
@@ -486,33 +495,6 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
     return f.to(device), scale
 
 
-def _span(t):
-    """First address of a tensor and the first behind it."""
-    n = sum((k - 1) * s for k, s in zip(t.shape, t.stride())) + 1 if t.numel() else 0
-    return t.data_ptr(), t.data_ptr() + n * t.element_size()
-
-
-def _apart(name, out, others, itself=None):
-    """Refuse an output that shares memory with `others` (and with `itself`,
-    unless it is that very tensor)."""
-    lo, hi = _span(out)
-    if itself is not None and not (itself.data_ptr() == lo and itself.stride() == out.stride()
-                                   and itself.dtype is out.dtype):
-        others = (*others, itself)
-    for t in others:
-        a, b = _span(t)
-        if lo < b and a < hi:
-            raise ValueError(f"{name}: shares memory with another argument")
-
-
-def _head_rows(t, name):
-    """Strides of a [T, H, d] view whose rows are dense and 16-byte aligned."""
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (s0 | s1) & 7 or t.data_ptr() & 15:
-        raise ValueError(f"{name}: dense rows, 16-byte aligned, strides multiples of 8 elements")
-    return s0, s1
-
-
 def qk_norm_rope(q, k, positions, inv_freq=None, *, interleaved: bool = False, rope_scale: float = 1.0,
                  q_weight=None, k_weight=None, eps: float = 1e-6, out=None, stream=None):
     """Norm of every query and key head and rotation by position.
@@ -526,89 +508,10 @@ def qk_norm_rope(q, k, positions, inv_freq=None, *, interleaved: bool = False, r
     calls do. `out` = (q_out, k_out), which may be q and k where they are
     contiguous fp16, and share no memory with the inputs otherwise.
     """
-    import torch
-
-    half = torch.float16
-    if not (isinstance(q, torch.Tensor) and isinstance(k, torch.Tensor) and q.dim() == 3 and k.dim() == 3):
-        raise ValueError("q: [T, Hq, d]; k: [T, Hkv, d]")
-    T, hq, d = q.shape
-    Tk, hkv, dk = k.shape
-    if Tk != T or dk != d:
-        raise ValueError("q: [T, Hq, d]; k: [T, Hkv, d] with the same T and d")
-    if d not in (64, 128, 256):
-        raise ValueError(f"head_dim: 64, 128 or 256, got {d}")
-    if not (hq and hkv):
-        raise ValueError("q, k: at least one head")
-    kind = q.dtype
-    if (kind is not half and kind is not torch.bfloat16) or k.dtype is not kind:
-        raise ValueError(f"q, k: both float16 or both bfloat16, got {q.dtype} and {k.dtype}")
-    q0, q1 = _head_rows(q, "q")
-    k0, k1 = _head_rows(k, "k")
-    _check(positions, "positions", torch.int32, numel=T)
-    rot = 0
-    if inv_freq is not None:
-        _check(inv_freq, "inv_freq", torch.float64)
-        rot = 2 * inv_freq.numel()
-        if rot > d:
-            raise ValueError(f"inv_freq: at most {d // 2} frequencies, got {rot // 2}")
-    w_type = None
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _check(w, name, kind if w.dtype is kind else (kind, torch.float32), numel=d)
-            if w.data_ptr() & 15:
-                raise ValueError(f"{name}: 16-byte aligned")
-            if w_type is not None and w_type is not w.dtype:
-                raise ValueError("q_weight, k_weight: the same dtype")
-            w_type = w.dtype
-    if not eps >= 0.0:
-        raise ValueError("eps: >= 0")
-    qo, ko = out if out is not None else (None, None)
-    if out is not None:
-        _check(qo, "out q", half, shape=(T, hq, d))
-        _check(ko, "out k", half, shape=(T, hkv, d))
-        _apart("out q", qo, (k, ko), q)
-        _apart("out k", ko, (q, qo), k)
-    dev = _one_device(("q", "k", "positions", "inv_freq", "q_weight", "k_weight", "out q", "out k"),
-                      (q, k, positions, inv_freq, q_weight, k_weight, qo, ko))
-    if _elsewhere(dev, stream):
-        with _launching(q.device, stream):
-            return qk_norm_rope(q, k, positions, inv_freq, interleaved=interleaved, rope_scale=rope_scale,
-                                q_weight=q_weight, k_weight=k_weight, eps=eps, out=out)
-    if out is None:
-        qo = torch.empty((T, hq, d), dtype=half, device=q.device)
-        ko = torch.empty((T, hkv, d), dtype=half, device=q.device)
-    tq_qk_norm_rope(q, k, TQ_F16 if kind is half else TQ_BF16, T, hq, hkv, d, q0, q1, k0, k1, positions, inv_freq,
-                    rot, interleaved, rope_scale, q_weight, k_weight, w_type is torch.float32, eps, qo, ko,
-                    _raw_stream(dev))
-    return qo, ko
-
-
-def _window_args(q, k_codec, v_codec, q_offsets, max_q, n_seq, hkv, window, sinks, out, workspace):
-    import torch
-
-    T, hq, d = q.shape
-    _check(q, "q", torch.float16, shape=(T, hq, k_codec.head_dim))
-    if d != v_codec.head_dim:
-        raise ValueError("k_codec, v_codec: the same head_dim")
-    if not (hkv > 0 and hq > 0 and hq % hkv == 0):
-        raise ValueError(f"q: a multiple of {hkv} heads, got {hq}")
-    if window is not None and int(window) < 1:
-        raise ValueError("window: None or at least 1")
-    if int(sinks) < 0:
-        raise ValueError("sinks: at least 0")
-    if q_offsets is None:
-        if T != n_seq or max_q not in (None, 1):
-            raise ValueError("q: one token per sequence where q_offsets is None")
-        max_q = 1
-    else:
-        _check(q_offsets, "q_offsets", torch.int32, numel=n_seq + 1)
-        if max_q is None or int(max_q) < 1:
-            raise ValueError("max_q: the largest number of tokens of a sequence")
-    if out is not None:
-        _check(out, "out", torch.float16, shape=(T, hq, d))
-    if workspace is not None:
-        _check(workspace, "workspace", torch.uint8)
-    return T, hq, d, int(max_q), 0 if window is None else int(window), int(sinks)
+    args = (q, k, positions, inv_freq, interleaved, rope_scale, q_weight, k_weight, eps, out)
+    if stream is not None:
+        return _on_stream(stream, "q", q, _calls().qk_norm_rope, *args)
+    return _calls().qk_norm_rope(*args)
 
 
 def attend_window(q, k_codec: TurboQuant, v_codec: TurboQuant, k_packed, k_norms, v_packed, v_norms, context_lens,
@@ -624,35 +527,11 @@ def attend_window(q, k_codec: TurboQuant, v_codec: TurboQuant, k_packed, k_norms
     one token per sequence). Returns o [T, Hq, d] fp16 (rows of tokens in no
     sequence are not written).
     """
-    import torch
-
-    if q.dim() != 3 or k_packed.dim() != 4:
-        raise ValueError("q: [T, Hq, d]; k_packed: [B, S, Hkv, Pk]")
-    B, s_max, hkv, _ = k_packed.shape
-    given = window  # as the caller has it, for a call made again inside another device or stream
-    T, hq, d, max_q, window, sinks = _window_args(q, k_codec, v_codec, q_offsets, max_q, B, hkv, window, sinks, out,
-                                                  workspace)
-    _check(k_packed, "k_packed", torch.uint8, shape=(B, s_max, hkv, k_codec.packed_bytes))
-    _check(v_packed, "v_packed", torch.uint8, shape=(B, s_max, hkv, v_codec.packed_bytes))
-    _check(k_norms, "k_norms", torch.float32, shape=(B, s_max, hkv))
-    _check(v_norms, "v_norms", torch.float32, shape=(B, s_max, hkv))
-    _check(context_lens, "context_lens", torch.int32, numel=B)
-    dev = _one_device(("q", "q_offsets", "out", "workspace", "k_packed", "v_packed", "k_norms", "v_norms",
-                       "context_lens"),
-                      (q, q_offsets, out, workspace, k_packed, v_packed, k_norms, v_norms, context_lens))
-    if _elsewhere(dev, stream):
-        with _launching(q.device, stream):
-            return attend_window(q, k_codec, v_codec, k_packed, k_norms, v_packed, v_norms, context_lens, given, sinks,
-                                 q_offsets, max_q, out, workspace)
-    if out is None:
-        out = torch.empty_like(q)
-    if workspace is None:
-        need = tq_attend_window_workspace_bytes(T, B, max_q, hq, hkv, d, s_max, window, sinks)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    tq_attend_window(k_codec.ctx, v_codec.ctx, q, T, B, q_offsets, max_q, hq, hkv, k_packed, k_norms, v_packed,
-                     v_norms, s_max, context_lens, window, sinks, out, workspace,
-                     0 if workspace is None else workspace.numel(), _raw_stream(dev))
-    return out
+    args = (q, k_codec.ctx.address, v_codec.ctx.address, k_packed, k_norms, v_packed, v_norms, False, None,
+            context_lens, window, sinks, q_offsets, max_q, out, workspace)
+    if stream is not None:
+        return _on_stream(stream, "q", q, _calls().attend_window, *args)
+    return _calls().attend_window(*args)
 
 
 def attend_window_paged(q, k_codec: TurboQuant, v_codec: TurboQuant, k_cache, k_norms, v_cache, v_norms,
@@ -662,66 +541,11 @@ def attend_window_paged(q, k_codec: TurboQuant, v_codec: TurboQuant, k_cache, k_
     block_tables [B, max_blocks] int32 as `attend_decode_paged`. Table entries
     of pages that no query sees are not read, so they may be negative
     (`pages_trim`)."""
-    import torch
-
-    if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2:
-        raise ValueError("q: [T, Hq, d]; k_cache: [num_blocks, 16, Hkv, Pk]; block_tables: [B, max_blocks]")
-    num_blocks, blk, hkv, _ = k_cache.shape
-    if blk != TQ_PAGE_BLOCK:
-        raise ValueError(f"cache blocks must hold {TQ_PAGE_BLOCK} positions")
-    B, max_blocks = block_tables.shape
-    given = window  # as the caller has it, for a call made again inside another device or stream
-    T, hq, d, max_q, window, sinks = _window_args(q, k_codec, v_codec, q_offsets, max_q, B, hkv, window, sinks, out,
-                                                  workspace)
-    _check(k_cache, "k_cache", torch.uint8, shape=(num_blocks, blk, hkv, k_codec.packed_bytes))
-    _check(v_cache, "v_cache", torch.uint8, shape=(num_blocks, blk, hkv, v_codec.packed_bytes))
-    _check(k_norms, "k_norms", torch.float32, shape=(num_blocks, blk, hkv))
-    _check(v_norms, "v_norms", torch.float32, shape=(num_blocks, blk, hkv))
-    _check(block_tables, "block_tables", torch.int32)
-    _check(context_lens, "context_lens", torch.int32, numel=B)
-    dev = _one_device(("q", "q_offsets", "out", "workspace", "k_cache", "v_cache", "k_norms", "v_norms",
-                       "block_tables", "context_lens"),
-                      (q, q_offsets, out, workspace, k_cache, v_cache, k_norms, v_norms, block_tables, context_lens))
-    if _elsewhere(dev, stream):
-        with _launching(q.device, stream):
-            return attend_window_paged(q, k_codec, v_codec, k_cache, k_norms, v_cache, v_norms, block_tables,
-                                       context_lens, given, sinks, q_offsets, max_q, out, workspace)
-    if out is None:
-        out = torch.empty_like(q)
-    if workspace is None:
-        need = tq_attend_window_workspace_bytes(T, B, max_q, hq, hkv, d, max_blocks * TQ_PAGE_BLOCK, window, sinks)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    tq_attend_window_paged(k_codec.ctx, v_codec.ctx, q, T, B, q_offsets, max_q, hq, hkv, k_cache, k_norms, v_cache,
-                           v_norms, num_blocks, block_tables, max_blocks, context_lens, window, sinks, out, workspace,
-                           0 if workspace is None else workspace.numel(), _raw_stream(dev))
-    return out
-
-
-def _page_state(block_tables, context_lens, refs, num_blocks):
-    """Checks of the tables of a paged cache; (rows, max_blocks)."""
-    import torch
-
-    _check(block_tables, "block_tables", torch.int32)
-    if block_tables.dim() != 2 or not block_tables.numel():
-        raise ValueError("block_tables: [rows, max_blocks]")
-    rows, max_blocks = block_tables.shape
-    if context_lens is not None:
-        _check(context_lens, "context_lens", torch.int32, numel=rows)
-    _check(refs, "refs", torch.int32)
-    if refs.dim() != 1 or not refs.numel() or (num_blocks is not None and refs.numel() != num_blocks):
-        raise ValueError(f"refs: one count per page ({num_blocks}), got {tuple(refs.shape)}")
-    return rows, max_blocks
-
-
-def _page_outputs(out, inputs, lists=(), more=()):
-    """Checks of page outputs: like the inputs, each of them its own input or
-    apart from everything else (`lists`: inputs without an output, `more`:
-    outputs without an input, whose sizes have been checked)."""
-    for i, (o, t) in enumerate(zip(out, inputs)):
-        _check(o, "out", t.dtype, shape=t.shape)
-        _apart("out", o, (*inputs[:i], *inputs[i + 1:], *out[:i], *out[i + 1:], *lists, *more), t)
-    for i, o in enumerate(more):
-        _apart("out", o, (*inputs, *lists, *more[:i], *more[i + 1:]))
+    args = (q, k_codec.ctx.address, v_codec.ctx.address, k_cache, k_norms, v_cache, v_norms, True, block_tables,
+            context_lens, window, sinks, q_offsets, max_q, out, workspace)
+    if stream is not None:
+        return _on_stream(stream, "q", q, _calls().attend_window, *args)
+    return _calls().attend_window(*args)
 
 
 def pages_trim(block_tables, context_lens, refs, window=None, sinks: int = 0, release=None, out=None, stream=None):
@@ -734,27 +558,10 @@ def pages_trim(block_tables, context_lens, refs, window=None, sinks: int = 0, re
     context_lens, refs), written to `out` where given (its tensors may be the
     inputs themselves).
     """
-    import torch
-
-    rows, max_blocks = _page_state(block_tables, context_lens, refs, None)
-    if window is not None and int(window) < 0:
-        raise ValueError("window: None or at least 0")
-    if int(sinks) < 0:
-        raise ValueError("sinks: at least 0")
-    if release is not None:
-        _check(release, "release", torch.bool if release.dtype is torch.bool else (torch.bool, torch.uint8), numel=rows)
-    if out is not None:
-        _page_outputs(out, (block_tables, context_lens, refs))
-    dev = _one_device(("block_tables", "context_lens", "refs", "release", "out", "out", "out"),
-                      (block_tables, context_lens, refs, release, *(out if out is not None else ())))
-    if _elsewhere(dev, stream):
-        with _launching(refs.device, stream):
-            return pages_trim(block_tables, context_lens, refs, window, sinks, release, out)
-    t, n, r = out if out is not None else (torch.empty_like(block_tables), torch.empty_like(context_lens),
-                                           torch.empty_like(refs))
-    tq_pages_trim(block_tables, t, context_lens, n, refs, r, rows, max_blocks, refs.numel(),
-                  -1 if window is None else int(window), int(sinks), release, _raw_stream(dev))
-    return t, n, r
+    args = (block_tables, context_lens, refs, window, sinks, release, out)
+    if stream is not None:
+        return _on_stream(stream, "refs", refs, _calls().pages_trim, *args)
+    return _calls().pages_trim(*args)
 
 
 class TQPagePools:
@@ -784,11 +591,7 @@ class TQPagePools:
         for i, t in enumerate(tensors):
             self._array[i].base = t.data_ptr()
             self._array[i].block_bytes = t.numel() // t.shape[0] * t.element_size()
-
-    def _on_mine(self, names, tensors):
-        dev = _one_device(names, tensors)
-        if dev != self._dev:
-            raise ValueError(f"tensors on cuda:{self._dev} like the pools, got cuda:{dev}")
+        self._mine = (ctypes.addressof(self._array), len(tensors), self.num_blocks, self._dev)
 
     def fork(self, block_tables, context_lens, refs, parents, children, out=None, workspace=None, stream=None):
         """Make row children[i] a copy of row parents[i]: the parent's full
@@ -796,31 +599,10 @@ class TQPagePools:
         free page. parents, children [n] int32; other tensors as `pages_trim`.
         A child's former pages are not given back (`pages_trim` first). Returns
         (block_tables, context_lens, refs)."""
-        import torch
-
-        rows, max_blocks = _page_state(block_tables, context_lens, refs, self.num_blocks)
-        n = parents.numel()
-        _check(parents, "parents", torch.int32)
-        _check(children, "children", torch.int32, numel=n)
-        if not n <= rows <= TQ_MAX_PAGE_ROWS:
-            raise ValueError(f"at most {rows} forks of at most {TQ_MAX_PAGE_ROWS} rows")
-        if out is not None:
-            _page_outputs(out, (block_tables, context_lens, refs), (parents, children))
-        if workspace is not None:
-            _check(workspace, "workspace", torch.uint8)
-        self._on_mine(("block_tables", "context_lens", "refs", "parents", "children", "workspace", "out", "out", "out"),
-                      (block_tables, context_lens, refs, parents, children, workspace,
-                       *(out if out is not None else ())))
-        if _elsewhere(self._dev, stream):
-            with _launching(refs.device, stream):
-                return self.fork(block_tables, context_lens, refs, parents, children, out, workspace)
-        t, c, r = out if out is not None else (torch.empty_like(block_tables), torch.empty_like(context_lens),
-                                               torch.empty_like(refs))
-        if workspace is None:
-            workspace = torch.empty(tq_pages_fork_workspace_bytes(n), dtype=torch.uint8, device=refs.device)
-        tq_pages_fork(self._array, len(self._array), self.num_blocks, block_tables, t, context_lens, c, refs, r, rows,
-                      max_blocks, parents, children, n, workspace, workspace.numel(), _raw_stream(self._dev))
-        return t, c, r
+        args = (*self._mine, block_tables, context_lens, refs, parents, children, out, workspace)
+        if stream is not None:
+            return _on_stream(stream, "refs", refs, _calls().pages_fork, *args)
+        return _calls().pages_fork(*args)
 
     def compact(self, block_tables, refs, out=None, workspace=None, stream=None):
         """Move the used pages (refs > 0) to the front of the pools. Returns
@@ -828,27 +610,7 @@ class TQPagePools:
         numbers, the moved counts, the new number of every page (-1: free) and
         the number of used pages [1] int32. `out` = (block_tables, refs, remap,
         used); the first two may be the inputs themselves."""
-        import torch
-
-        rows, max_blocks = _page_state(block_tables, None, refs, self.num_blocks)
-        if rows > TQ_MAX_PAGE_ROWS:
-            raise ValueError(f"block_tables: at most {TQ_MAX_PAGE_ROWS} rows")
-        if out is not None:
-            _check(out[2], "out remap", torch.int32, numel=self.num_blocks)
-            _check(out[3], "out used", torch.int32, numel=1)
-            _page_outputs(out[:2], (block_tables, refs), (), out[2:])
-        if workspace is not None:
-            _check(workspace, "workspace", torch.uint8)
-        self._on_mine(("block_tables", "refs", "workspace", "out", "out", "out", "out"),
-                      (block_tables, refs, workspace, *(out if out is not None else ())))
-        if _elsewhere(self._dev, stream):
-            with _launching(refs.device, stream):
-                return self.compact(block_tables, refs, out, workspace)
-        t, r, m, u = out if out is not None else (torch.empty_like(block_tables), torch.empty_like(refs),
-                                                  torch.empty_like(refs), refs.new_empty(1))
-        if workspace is None:
-            workspace = torch.empty(tq_pages_compact_workspace_bytes(self.num_blocks), dtype=torch.uint8,
-                                    device=refs.device)
-        tq_pages_compact(self._array, len(self._array), self.num_blocks, block_tables, t, refs, r, rows, max_blocks,
-                         m, u, workspace, workspace.numel(), _raw_stream(self._dev))
-        return t, r, m, u
+        args = (*self._mine, block_tables, refs, out, workspace)
+        if stream is not None:
+            return _on_stream(stream, "refs", refs, _calls().pages_compact, *args)
+        return _calls().pages_compact(*args)

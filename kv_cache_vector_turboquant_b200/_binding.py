@@ -11,7 +11,6 @@ raises ``ImportError`` if the library has not been built
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtq.so")
@@ -166,6 +165,10 @@ class Ctx:
         self._h = ctypes.c_void_p(handle)
 
     @property
+    def address(self) -> int:
+        return self._h.value
+
+    @property
     def handle(self) -> ctypes.c_void_p:
         return self._h
 
@@ -295,7 +298,6 @@ def tq_qk_norm_rope(q, k, dtype: int, n_tok: int, hq: int, hkv: int, head_dim: i
                                 q_out.data_ptr(), k_out.data_ptr(), _stream(stream)), "tq_qk_norm_rope")
 
 
-@functools.lru_cache(maxsize=256)  # a function of the sizes alone; a decode loop asks for the same ones
 def tq_attend_window_workspace_bytes(n_tok: int, B: int, max_q: int, hq: int, hkv: int, head_dim: int, s_max: int,
                                      window: int, sinks: int) -> int:
     return _lib.tq_attend_window_workspace_bytes(n_tok, B, max_q, hq, hkv, head_dim, s_max, window, sinks)

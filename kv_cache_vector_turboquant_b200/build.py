@@ -1,4 +1,5 @@
-"""Build libtq.so in-tree with nvcc for sm_100a.
+"""Build libtq.so in-tree with nvcc for sm_100a, and _ops.so (argument checks and
+calls for PyTorch tensors, linked against libtq.so and torch) beside it.
 
 Usage: ``python kv_cache_vector_turboquant_b200/build.py [--force] [-j N]`` (run as a
 script: importing the package would load the library being built).
@@ -12,10 +13,12 @@ ships.
 from __future__ import annotations
 
 import argparse
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -25,11 +28,13 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtq.so")
 TEST_LIB = os.path.join(PKG, "libtq_test.so")
+OPS_LIB = os.path.join(PKG, "_ops.so")
 
 SOURCES = ["tq_host.cpp", "tq_device.cu", "tq_encode.cu", "tq_encode_tc.cu", "tq_decode.cu", "tq_decode_tc.cu", "tq_attend.cu", "tq_attend_fast.cu", "tq_attend_static.cu", "tq_mma_check.cu", "tq_norm_rope.cu", "tq_attend_window.cu", "tq_attend_window_tc.cu", "tq_pages.cu"]
 # test hooks (include/tq_test.h): a separate library, linked against libtq.so,
 # that the product path never loads
 TEST_SOURCES = ["tq_test_hooks.cpp", "tq_test_umma.cu"]
+OPS_SOURCES = ["tq_torch.cpp"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 
@@ -39,6 +44,14 @@ def _nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def _torch() -> str:
+    """Directory of the installed torch (found without importing it)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch not found")
+    return spec.submodule_search_locations[0]
 
 
 def _headers() -> list[str]:
@@ -55,13 +68,14 @@ def _stale(target: str, deps: list[str]) -> bool:
 
 
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
-    """Compile every source for sm_100a, link libtq.so and libtq_test.so;
-    return the path of libtq.so."""
+    """Compile every source for sm_100a, link libtq.so, libtq_test.so and
+    _ops.so; return the path of libtq.so."""
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     headers = _headers()
-    objs, test_objs, todo = [], [], []
-    for srcs, out in ((SOURCES, objs), (TEST_SOURCES, test_objs)):
+    objs, test_objs, ops_objs, todo = [], [], [], []
+    torch = _torch()
+    for srcs, out in ((SOURCES, objs), (TEST_SOURCES, test_objs), (OPS_SOURCES, ops_objs)):
         for src in srcs:
             path = os.path.join(CSRC, src)
             obj = os.path.join(BUILD, src + ".o")
@@ -74,6 +88,8 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         cmd = [nvcc] + ARCH + FLAGS + ["-c", path, "-o", obj]
         if path.endswith(".cpp"):
             cmd = [nvcc] + FLAGS + ["-x", "c++", "-c", path, "-o", obj]
+            if obj in ops_objs:
+                cmd += ["-I" + os.path.join(torch, "include"), "-I" + sysconfig.get_paths()["include"]]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
@@ -99,6 +115,15 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         if r.returncode != 0:
             raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, TEST_LIB)
+    if force or todo or _stale(OPS_LIB, ops_objs + [LIB]):
+        tmp = OPS_LIB + ".tmp"
+        cmd = [nvcc, "-shared", "-cudart", "none", "-o", tmp] + ops_objs + [
+            "-L" + PKG, "-ltq", "-Xlinker", "-rpath", "-Xlinker", "$ORIGIN", "-L" + os.path.join(torch, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, OPS_LIB)
     return LIB
 
 
