@@ -723,15 +723,26 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_consta
 // Measured, 8 sequences of up to 8000 positions (this kernel / that one): 16
 // rows 66 / 114 us, 40 rows (4 kv heads) 81 / 75, 64 rows 220 / 119.
 constexpr int64_t AW_TC_ROWS = 40;
-
-static bool window_tc(int hq, int hkv, int max_q) { return (int64_t)max_q * (hq / hkv) >= AW_TC_ROWS; }
+// With at most 128 of them, and no more than one row tile of head_dim 64 or 128
+// in use, the tensor-memory kernel's two row tiles hold the same rows and take
+// alternate tiles of positions, each as a split of its own, from this many
+// positions on. Measured, d = 128 (one row tile / halves): 8 sequences of 8000
+// positions 78 / 68 us, 32 sequences of 2048 135 / 130, of 1024 86 / 86, of
+// 512 63 / 68 (twice the partial results to merge).
+constexpr int64_t AW_HALVES = 1024;
 
 // Splits of a call, from the sizes alone, so that the workspace is too: this
 // kernel, enough warps to fill the SMs twice over, at least one step of 32
 // positions each; the tensor-memory kernel, one CTA per SM, at least four
 // tiles of 64 each.
-static int window_splits(int B, int hq, int hkv, int max_q, int d, int64_t s_max, int64_t window, int64_t sinks) {
-  const bool tc = window_tc(hq, hkv, max_q);
+struct WindowPlan {
+  int n_split;
+  bool tc, halves;
+};
+static WindowPlan window_plan(int B, int hq, int hkv, int max_q, int d, int64_t s_max, int64_t window, int64_t sinks) {
+  WindowPlan p{};
+  p.tc = (int64_t)max_q * (hq / hkv) >= AW_TC_ROWS;
+  const bool tc = p.tc;
   const int64_t rows = (int64_t)max_q * (hq / hkv);
   const int64_t rt = tc ? tq_window_tc_rows(d) : rows > 4 && d <= 128 ? 8 : 4;
   const int64_t tiles = (rows + rt - 1) / rt;
@@ -740,7 +751,10 @@ static int window_splits(int B, int hq, int hkv, int max_q, int d, int64_t s_max
   if (window > 0) seen = std::min(seen, window + sinks + max_q + 2 * ATT_BLOCK);
   const int64_t steps = tc ? (seen + 255) / 256 : (seen + AW_TILE - 1) / AW_TILE;
   const int64_t slots = tc ? 148 : 148 * (d * rt <= 512 ? 16 : 8);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(slots / units, steps));
+  p.n_split = (int)std::max<int64_t>(1, std::min<int64_t>(slots / units, steps));
+  p.halves = tc && d <= 128 && rows <= 128 && seen >= AW_HALVES;
+  if (p.halves) p.n_split *= 2;
+  return p;
 }
 
 template <int D, int KB, int VB, int NT>
@@ -790,7 +804,7 @@ cudaError_t tq_launch_window_combine(const AwArgs& a, int d, cudaStream_t st) {
 
 size_t tq_attend_window_workspace_impl(int64_t n_tok, int B, int max_q, int hq, int hkv, int head_dim, int64_t s_max,
                                        int64_t window, int64_t sinks) {
-  const int ns = window_splits(B, hq, hkv, max_q, head_dim, s_max, window, sinks);
+  const int ns = window_plan(B, hq, hkv, max_q, head_dim, s_max, window, sinks).n_split;
   if (ns == 1) return 0;
   const size_t rows = (size_t)n_tok * hq * ns;
   return 2 * align16(rows * 4) + rows * (size_t)head_dim * 4;
@@ -834,7 +848,9 @@ tq_status tq_launch_attend_window(const tq_ctx* k, const tq_ctx* v, const void* 
   a.g = hq / hkv;
   a.window = window <= 0 || window > INT_MAX ? INT_MAX : (int)window;
   a.sinks = (int)std::min<int64_t>(sinks, INT_MAX);
-  a.n_split = window_splits(B, hq, hkv, max_q, d, s_max, window, sinks);
+  const WindowPlan plan = window_plan(B, hq, hkv, max_q, d, s_max, window, sinks);
+  a.n_split = plan.n_split;
+  a.halves = plan.halves;
   const size_t rows = (size_t)n_tok * hq * a.n_split;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.ws_m = reinterpret_cast<float*>(ws);
@@ -843,9 +859,8 @@ tq_status tq_launch_attend_window(const tq_ctx* k, const tq_ctx* v, const void* 
   a.err = tq_error_word();
   if (!a.err) return TQ_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  a.wait_limit = TQ_WAIT_LIMIT_CYCLES;
   cudaError_t e = cudaErrorInvalidValue;
-  if (window_tc(hq, hkv, max_q)) {
+  if (plan.tc) {
     e = tq_launch_window_tc(a, d, k->bits, v->bits, st);
     if (e == cudaSuccess && a.n_split > 1) e = tq_launch_window_combine(a, d, st);
     if (e == cudaErrorNotSupported) return TQ_ERR_UNSUPPORTED;

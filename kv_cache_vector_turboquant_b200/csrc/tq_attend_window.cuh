@@ -36,11 +36,11 @@ struct AwArgs {
   int B, max_q, hq, hkv, g;
   int window, sinks;  // window: INT_MAX for none
   int n_split;
+  int halves;     // tcgen05 kernel: a CTA's two row tiles hold the same rows, two splits
   float* ws_m;    // [n_tok * hq, n_split] running max (log2 domain)
   float* ws_l;    // [n_tok * hq, n_split] sum of weights
   float* ws_acc;  // [n_tok * hq, n_split, D] rotated accumulator
   uint32_t* err;
-  long long wait_limit;
 };
 
 // The sequence's first query token, its number of query tokens (0: nothing to
@@ -114,7 +114,6 @@ TQ_DEV int64_t aw_entry_row(const AwArgs& a, int b, int entry) {
   }
   return page * ATT_BLOCK;
 }
-TQ_DEV int64_t aw_block_row(const AwArgs& a, int b, int j) { return aw_entry_row(a, b, aw_block_entry(a, b, j)); }
 
 TQ_DEV float aw_exp2(float x) {
   float y;

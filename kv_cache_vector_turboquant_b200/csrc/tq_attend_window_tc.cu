@@ -26,7 +26,10 @@
 //    (exact: sum and accumulator share it), so the accumulator is rescaled
 //    rarely.
 // Scores are double-buffered: the next tile's S is computed while the
-// softmax works on the current one.
+// softmax works on the current one. Calls whose rows fit one row tile may have
+// it twice (`halves`): both hold the same rows, and each walks over every
+// other tile of positions as a split of its own, so that two softmax groups
+// work on one set of rows.
 //
 // Per row tile and 64 positions: 4 x 64 x 128 x d multiply-adds (scores and
 // values, each with its remainder: 512 tensor cycles at d = 128), an
@@ -41,7 +44,7 @@
 namespace tq {
 
 constexpr int TW_TP = 64;       // positions of a tile
-constexpr int TW_SLOTS = 4;     // norm slots in flight
+constexpr int TW_SLOTS = 8;     // norm slots in flight
 constexpr int TW_TMEM = 512;
 
 // Norms and positions of one tile.
@@ -50,8 +53,7 @@ struct TwSlot {
   float nv[TW_TP];   // times the power of two of the tile
   int blk_t[4];      // first position of each 16-position block (INT_MAX - 64: none)
   int t_min, t_max;  // first and last position
-  float v_fix;       // this tile's power of two over the previous tile's
-  float v_inv;       // its inverse
+  float v_up, v_inv; // this tile's power of two and its inverse
   uint32_t odd[2];   // positions whose value norm is infinite or NaN (0 in nv)
   int pad[2];
 };
@@ -187,7 +189,8 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
   extern __shared__ uint8_t raw_smem[];
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int b = blockIdx.z;
-  const int split = blockIdx.x / a.hkv, hk = blockIdx.x - split * a.hkv;
+  const int c_split = blockIdx.x / a.hkv, hk = blockIdx.x - c_split * a.hkv;
+  const bool halves = MT == 2 && a.halves;
   const AwSeq sq = aw_sequence(a, b, blockIdx.x == 0 && blockIdx.y == 0 && tid == 0);
   const int rows = sq.n * a.g, r0 = blockIdx.y * (128 * MT);
   if (r0 >= rows) return;
@@ -196,8 +199,9 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
   const int r1 = min(r0 + 128 * MT, rows) - 1;
   const int p_hi = aw_position(sq, r1 / a.g);
   const AwBlocks bl = aw_blocks(aw_position(sq, r0 / a.g), p_hi, a.window, a.sinks);
-  const int tiles = (bl.n + 3) / 4, share = (tiles + a.n_split - 1) / a.n_split;
-  const int tile0 = split * share, cnt = max(0, min(share, tiles - tile0));
+  const int tiles = (bl.n + 3) / 4, n_cta = halves ? a.n_split / 2 : a.n_split;
+  const int share = (tiles + n_cta - 1) / n_cta;
+  const int tile0 = c_split * share, cnt = max(0, min(share, tiles - tile0));
 
   const uint32_t raw = smem_u32(raw_smem), base = (raw + 1023u) & ~1023u;
   uint8_t* sm = raw_smem + (base - raw);
@@ -208,9 +212,9 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
   if (tid == 0) {
     for (int i = 0; i < NBUF; ++i) {
       mbar_init(k_full + 8 * i, 128 + 32);  // the key warps and the norm warp
-      mbar_init(k_empty + 8 * i, MT);
+      mbar_init(k_empty + 8 * i, halves ? 1 : MT);  // the issuers that read it
       mbar_init(v_full + 8 * i, 128);
-      mbar_init(v_empty + 8 * i, MT);
+      mbar_init(v_empty + 8 * i, halves ? 1 : MT);
     }
     for (int i = 0; i < TW_SLOTS; ++i) mbar_init(n_full + 8 * i, 32);
     for (int i = 0; i < 2 * MT; ++i) {
@@ -412,16 +416,17 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
       const uint32_t s0 = tmem + 256u * t, o0 = s0 + 128u;
       const uint64_t q_desc = umma_desc_sw128(base + C::Q0 + 2 * t * C::Q_PART);
       const uint64_t k_desc = umma_desc_sw128(base + C::K0), v_desc = umma_desc_sw128(base + C::V0);
-      const bool active = r0 + 128 * t < rows;  // a row tile without rows only signals
+      const bool active = halves || r0 + 128 * t < rows;  // a row tile without rows only signals
+      const int n = halves ? (cnt + 1 - t) / 2 : cnt;
       // the whole warp waits, one elected lane issues
       bool ok = __all_sync(FULL, tw_wait(q_full + 8 * t, 0, TW_TRIES));
-      for (int i = 0; i <= cnt && ok; ++i) {
-        if (i < cnt) {
-          const int buf = i % NBUF;
+      for (int j = 0; j <= n && ok; ++j) {  // this row tile's j-th tile of positions
+        if (j < n) {
+          const int i = halves ? 2 * j + t : j, buf = i % NBUF;
           ok = __all_sync(FULL, tw_wait(k_full + 8 * buf, (i / NBUF) & 1, TW_TRIES));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t s = s0 + 64u * (i & 1);
+          const uint32_t s = s0 + 64u * (j & 1);
           if (elect_one()) {
             if (active) {
               const uint64_t kd = k_desc + ((uint32_t)(buf * C::KV) >> 4);
@@ -432,14 +437,14 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
                   umma_f16(s, q_desc + ((part * C::Q_PART + (ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
                            kd + (((ks >> 2) * (TW_TP * 128) + (ks & 3) * 32) >> 4), ID_S, part + ks > 0);
             }
-            umma_commit(s_full + 16 * t + 8 * (i & 1));
+            umma_commit(s_full + 16 * t + 8 * (j & 1));
             umma_commit(k_empty + 8 * buf);
           }
           __syncwarp();
         }
-        if (i > 0) {
-          const int u = i - 1, buf = u % NBUF;
-          ok = __all_sync(FULL, tw_wait(v_full + 8 * buf, (u / NBUF) & 1, TW_TRIES) &&
+        if (j > 0) {
+          const int u = j - 1, i = halves ? 2 * u + t : u, buf = i % NBUF;
+          ok = __all_sync(FULL, tw_wait(v_full + 8 * buf, (i / NBUF) & 1, TW_TRIES) &&
                                     tw_wait(p_full + 16 * t + 8 * (u & 1), (u >> 1) & 1, TW_TRIES));
           if (!ok) break;
           tc_fence_after();
@@ -466,8 +471,9 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
       if (!tw_wait(mma_end + 8 * t, 0, TW_TRIES) && lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
     } else if (t == 2) {
       // ---- norms and positions of the tiles, two positions per lane. A slot is
-      // free again when the product two tiles back has read its keys (its
-      // issuer had the weights of the tile four back).
+      // free again when the product two tiles back has read its keys: its
+      // issuer had the weights of the tile two before that one in its row
+      // tile's order, which is at most six tiles back.
       const int q = lane >> 4;
       float nk[2], nv[2];
       int next[2];
@@ -514,14 +520,9 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
         for (int m = 16; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL, most, m));
         t_min = min(t_min, __shfl_xor_sync(FULL, t_min, 16));
         t_max = max(t_max, __shfl_xor_sync(FULL, t_max, 16));
-        float fix = 1.f;
         if (most > v_most) {
           v_most = most;
-          float inv;
-          const float up = aw_pow2_for<5>(most, inv);  // weights reach 2^8: 2^14 in fp16
-          fix = up * v_inv;
-          v_up = up;
-          v_inv = inv;
+          v_up = aw_pow2_for<5>(most, v_inv);  // weights reach 2^8: 2^14 in fp16
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
         if (lane == 0) {
           s.t_min = t_min;
           s.t_max = t_max;
-          s.v_fix = fix;
+          s.v_up = v_up;
           s.v_inv = v_inv;
         }
         if (i + 1 < cnt) fetch(i + 1);
@@ -546,14 +547,14 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
     regs_up<C::R_SM>();
     // ---- rotated queries, one row per softmax thread
     const int mt = warp >> 2;  // row tile
-    const int r_tile = tid & 127, r = r0 + tid;
+    const int r_tile = tid & 127, r_cta = halves ? r_tile : tid, r = r0 + r_cta;
     const bool row_ok = r < rows;
     const int q_i = row_ok ? r / a.g : 0, q_h = row_ok ? r - q_i * a.g : 0;
     const int64_t out_row = (sq.q0 + q_i) * a.hq + hk * a.g + q_h;
     float row_inv = 1.f;
     if (row_ok) {
-      const uint8_t* src = sm + C::K0 + tid * (2 * D);
-      const int sw = (tid & 7) << 4;
+      const uint8_t* src = sm + C::K0 + r_cta * (2 * D);
+      const int sw = (r_cta & 7) << 4;
       float ss = 0.f;
 #pragma unroll 4
       for (int e = 0; e < D / 8; ++e) {
@@ -618,14 +619,16 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
     // ---- softmax of one row per thread
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s0 = tmem + 256u * mt + lane_base, o0 = s0 + 128u;
-    const int rw0 = r0 + 32 * warp, rw1 = min(rw0 + 31, rows - 1);  // rows of this warp
+    const int rw0 = r0 + 32 * (halves ? warp & 3 : warp), rw1 = min(rw0 + 31, rows - 1);  // rows of this warp
     const bool any_row = rw0 < rows;
     const int pw_lo = any_row ? aw_position(sq, rw0 / a.g) : -1, pw_hi = any_row ? aw_position(sq, rw1 / a.g) : -1;
     const int p_row = row_ok ? aw_position(sq, q_i) : pw_hi;
     float m_ref = -INFINITY, l_sum = 0.f, v_inv = 1.f;
     bool ok = true;
-    for (int i = 0; i < cnt; ++i) {
-      ok = tw_wait(s_full + 16 * mt + 8 * (i & 1), (i >> 1) & 1, TW_TRIES) &&
+    const int n = halves ? (cnt + 1 - mt) / 2 : cnt;
+    for (int j = 0; j < n; ++j) {
+      const int i = halves ? 2 * j + mt : j;
+      ok = tw_wait(s_full + 16 * mt + 8 * (j & 1), (j >> 1) & 1, TW_TRIES) &&
            tw_wait(n_full + 8 * (i % TW_SLOTS), (i / TW_SLOTS) & 1, TW_TRIES);
       ok = __all_sync(FULL, ok);
       if (!ok) {
@@ -633,7 +636,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t sp = s0 + 64u * (i & 1);
+      const uint32_t sp = s0 + 64u * (j & 1);
       if (any_row) {
         const TwSlot& slot = reinterpret_cast<const TwSlot*>(sm + C::N0)[i % TW_SLOTS];
         float x[64];
@@ -679,7 +682,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
         const float mx = fmaxf(tw_max3(mx0, mx1, mx2), mx3) * row_inv;
         // the reference follows the maximum when it is exceeded by 2^8
         const bool move = mx > m_ref + 8.0f || (m_ref == -INFINITY && mx != -INFINITY);
-        const float v_fix = slot.v_fix;
+        const float v_fix = slot.v_up * v_inv;  // over the power of two of the tile before
         v_inv = slot.v_inv;
         float fix = v_fix;
         if (move) {
@@ -688,13 +691,13 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
           fix *= f;
           m_ref = mx;
         }
-        if (i > 0 && __any_sync(FULL, move || v_fix != 1.0f)) {
+        if (j > 0 && __any_sync(FULL, move || v_fix != 1.0f)) {
           // the previous product must be in the accumulator before it is
           // rescaled. (Even and odd tiles have barriers of their own: a wait
           // may be the first in many tiles, and this one's earlier phases
-          // ended before the scores of tile i - 1 were complete.)
+          // ended before the scores of tile j - 1 were complete.)
           const bool done = __all_sync(
-              FULL, tw_wait(o_done + 16 * mt + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, TW_TRIES));
+              FULL, tw_wait(o_done + 16 * mt + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, TW_TRIES));
           if (!done) {
             if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
             ok = false;
@@ -724,16 +727,16 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
         tmem_wait_st();
       }
       tc_fence_before();
-      mbar_arrive(p_full + 16 * mt + 8 * (i & 1));
+      mbar_arrive(p_full + 16 * mt + 8 * (j & 1));
     }
     // ---- results
-    if (ok && cnt > 0) {
+    if (ok && n > 0) {
       ok = __all_sync(FULL, tw_wait(mma_end + 8 * mt, 0, TW_TRIES));  // every product is done
       if (!ok && lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
       tc_fence_after();
     }
     if (any_row && ok) {
-      const int64_t idx = out_row * a.n_split + split;
+      const int64_t idx = out_row * a.n_split + (halves ? 2 * c_split + mt : c_split);
       if (a.n_split > 1 && row_ok) {
         a.ws_m[idx] = m_ref;
         a.ws_l[idx] = l_sum;
@@ -749,7 +752,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
         float x[64];
 #pragma unroll
         for (int e = 0; e < 64; ++e) x[e] = 0.f;
-        if (cnt > 0) {
+        if (n > 0) {
 #pragma unroll 1
           for (int m = a.n_split > 1 ? hf : 0; m < (a.n_split > 1 ? hf + 1 : D / 64); ++m) {
             const float sg = a.n_split > 1 || !(__popc(m & hf) & 1) ? 1.f : -1.f;
@@ -806,7 +809,7 @@ static cudaError_t launch_tc_t(const AwArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = aw_allow_smem(reinterpret_cast<const void*>(window_tc_kernel<D, KB, VB>), C::BYTES, done);
   if (e != cudaSuccess) return e;
-  const int64_t gx = (int64_t)a.n_split * a.hkv, gy = ((int64_t)a.max_q * a.g + 128 * C::MT - 1) / (128 * C::MT);
+  const int64_t gx = (int64_t)(a.halves ? a.n_split / 2 : a.n_split) * a.hkv, gy = ((int64_t)a.max_q * a.g + 128 * C::MT - 1) / (128 * C::MT);
   if (gx > 0x7fffffff || gy > 65535) return cudaErrorNotSupported;
   window_tc_kernel<D, KB, VB><<<dim3((unsigned)gx, (unsigned)gy, a.B), C::WARPS * 32, C::BYTES, st>>>(a);
   return cudaGetLastError();

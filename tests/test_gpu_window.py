@@ -69,6 +69,11 @@ CASES = [
     (128, 4, 3, 8, 2, 260, [(130, 260), (40, 41), (1, 200)], 60, 20),
     (64, 4, 2, 8, 1, 200, [(140, 200), (17, 17)], None, 0),
     (256, 4, 4, 4, 1, 150, [(70, 150)], 50, 3),
+    # 40 to 128 query rows per kv head over long contexts
+    (128, 4, 2, 32, 8, 1100, [(16, 1100), (11, 64), (1, 700), (0, 5), (16, 129)], None, 0),
+    (128, 3, 4, 8, 1, 900, [(16, 900), (16, 16)], 700, 70),
+    (64, 2, 2, 40, 1, 1500, [(3, 1500), (1, 65), (2, 1409)], None, 3),
+    (128, 4, 3, 5, 1, 1029, [(25, 1029)], None, 0),
 ]
 
 
