@@ -386,8 +386,8 @@ size_t tq_attend_window_workspace_bytes(int64_t n_tok, int B, int max_q, int hq,
  *               is fine). NULL: one token per sequence (n_tok == B, max_q 1).
  *               A sequence whose offsets leave [0, n_tok], decrease or exceed
  *               max_q is left out and flagged with TQ_DEVERR_ROW_RANGE. Rows
- *               of tokens in no sequence are not written (a token in two, after
- *               such offsets, gets the row of either).
+ *               of tokens in no sequence are not written (the row of a token
+ *               in two, after such offsets, is unspecified).
  *   context_lens device, [B] int32: L, the query tokens included. <= 0 gives
  *               zero rows; > s_max is clamped and flagged with
  *               TQ_DEVERR_POS_RANGE.

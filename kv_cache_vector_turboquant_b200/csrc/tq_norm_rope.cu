@@ -13,8 +13,14 @@
 // positions of a few thousand on; in f64 a position of 2^31 leaves 4e-8
 // turns), and sincospif takes the fraction.
 //
-// Bound: 2 B read and 2 B written per coordinate, if the instructions stay
-// below about 100 per warp and pass (two rows of 128). A CTA takes the rows of
+// Bound: 2 B read and 2 B written per coordinate. Measured, 8191 tokens of 40
+// heads of 128 bf16 coordinates with norm and 64 of them rotated (168 MB):
+// 36.9 us, 4.5 TB/s (25.5 us at a plain copy's rate); the schedulers issue 78 %
+// of their slots, about 154 warp instructions per pass (two rows of 128), so
+// instructions are the bound there. 16 tokens take 4.2 us, a launch's latency
+// and the chain position -> angle -> row.
+//
+// A CTA takes the rows of
 // up to 8 tokens, all queries or all keys: its threads first make the tokens'
 // angles (one or two each, (s cos, s sin) in shared memory), then pass over the
 // rows together, each stepping its own pointers. A lane holds 8 neighbouring

@@ -96,6 +96,10 @@ def test_window_refusals(K):
     _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx.long()), "context_lens: dtype")
     _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, window=0), "window")
     _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, sinks=-1), "sinks")
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, window=2.5), "window")
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, window=1 << 70), "window")
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, q_offsets=off, max_q="2"), "max_q")
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, [0, 0]), "context_lens: a torch tensor")
     _raises(lambda: f(torch.cat([q, q]), kc, vc, kp, kn, vp, vn, ctx), "one token per sequence")
     _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, max_q=2), "one token per sequence")
     _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, q_offsets=off), "max_q")
@@ -177,6 +181,7 @@ def test_abi_refusals(K):
     assert ws(2, 2, 1, 4, 2, 128, 64, 0, 0) > 0 and ws(2, 2, 1, 4, 3, 128, 64, 0, 0) == ws(0, 2, 1, 4, 2, 128, 64, 0, 0) == 0
     # the window bounds the splits, and so the workspace
     assert ws(2, 2, 1, 4, 2, 128, 1 << 20, 100, 4) < ws(2, 2, 1, 4, 2, 128, 1 << 20, 0, 0)
+    assert ws(2, 2, 1, 4, 2, 128, 1 << 20, (1 << 63) - 1, (1 << 63) - 1) == ws(2, 2, 1, 4, 2, 128, 1 << 20, 0, 0)
 
     def pg(nb=8, bt=p, mb=2, win=1, sinks=0):
         return L.tq_pages_trim(bt, p, p, p, p, p, 3, mb, nb, win, sinks, None, None)
