@@ -394,7 +394,8 @@ size_t tq_attend_window_workspace_bytes(int64_t n_tok, int B, int max_q, int hq,
  *   window      >= 1, or <= 0 for no limit.   sinks: >= 0.
  *   k_cache ... as tq_attend_decode: [B, s_max, hkv, P] and norms
  *               [B, s_max, hkv]; positions that no query sees are not read.
- *   out_f16     device, [n_tok, hq, d] fp16 out, 16-byte aligned.
+ *   out_f16     device, [n_tok, hq, d] fp16 out, 16-byte aligned; may be
+ *               q_f16 itself, and overlaps nothing else.
  *   workspace   at least tq_attend_window_workspace_bytes(...) bytes, 16-byte
  *               aligned (NULL if that is 0); contents on entry do not matter.
  * Any hq that is a multiple of hkv; hkv at most 65536, s_max below 2^31 - 256,

@@ -525,7 +525,8 @@ def attend_window(q, k_codec: TurboQuant, v_codec: TurboQuant, k_packed, k_norms
     keys and values are in the cache); q_offsets [B + 1] int32: sequence b's
     tokens are q[q_offsets[b]:q_offsets[b + 1]], at most max_q of them (None:
     one token per sequence). Returns o [T, Hq, d] fp16 (rows of tokens in no
-    sequence are not written).
+    sequence are not written). `out` may be q itself and shares no memory with
+    anything else.
     """
     args = (q, k_codec.ctx.address, v_codec.ctx.address, k_packed, k_norms, v_packed, v_norms, False, None,
             context_lens, window, sinks, q_offsets, max_q, out, workspace)

@@ -466,8 +466,8 @@ __global__ void __launch_bounds__(AwCfg<D, KB, VB, NT>::WARPS * 32, 1)
 #pragma unroll
           for (int j = 0; j < NT; ++j)
             if (!aw_visible(t_blk[h] + gq + 8 * r, p_row[j], a.window, a.sinks)) sc[j][h][r] = -INFINITY;
-          // a norm that no row sees takes no part (it may be infinite or NaN)
-          if (t_blk[h] + gq + 8 * r > p_hi) nv[h][r] = 0.f;
+          // a norm that no row sees takes no part in the power of two, whatever it is
+          if (!aw_seen(t_blk[h] + gq + 8 * r, p_lo, p_hi, a.window, a.sinks)) nv[h][r] = 0.f;
         }
     }
     // ---- a larger value norm than any before moves their power of two

@@ -78,6 +78,10 @@ TQ_DEV AwSeq aw_sequence(const AwArgs& a, int b, bool report) {
 // t > p - window).
 TQ_DEV int aw_position(const AwSeq& s, int i) { return max(s.ctx - s.n + i, -1); }
 TQ_DEV bool aw_visible(int t, int p, int window, int sinks) { return t <= p && (t < sinks || t > p - window); }
+// Whether one of the queries at positions p_lo..p_hi sees position t.
+TQ_DEV bool aw_seen(int t, int p_lo, int p_hi, int window, int sinks) {
+  return t <= p_hi && (t < sinks || t > p_lo - window);
+}
 
 // The 16-position blocks that queries at positions p_lo..p_hi see together:
 // the sinks' blocks [0, n_sink), then the window's from w0 on; n in all.

@@ -205,8 +205,8 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
 
   // ---- the tiles of this CTA
   const int r1 = min(r0 + 128 * MT, rows) - 1;
-  const int p_hi = aw_position(sq, r1 / a.g);
-  const AwBlocks bl = aw_blocks(aw_position(sq, r0 / a.g), p_hi, a.window, a.sinks);
+  const int p_lo = aw_position(sq, r0 / a.g), p_hi = aw_position(sq, r1 / a.g);
+  const AwBlocks bl = aw_blocks(p_lo, p_hi, a.window, a.sinks);
   const int tiles = (bl.n + 3) / 4, n_cta = halves ? a.n_split / 2 : a.n_split;
   const int share = (tiles + n_cta - 1) / n_cta;
   const int tile0 = c_split * share, cnt = max(0, min(share, tiles - tile0));
@@ -518,8 +518,10 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
         for (int h = 0; h < 2; ++h) {
           const int m = 4 * (tile0 + i) + 2 * h + q;
           const int at = m < bl.n ? aw_block(bl, m) * ATT_BLOCK : INT_MAX - 64;
+          // a norm that no row sees takes no part in the power of two, whatever it is
+          if (!aw_seen(at + (lane & 15), p_lo, p_hi, a.window, a.sinks)) nv[h] = 0.f;
           const float v = fabsf(nv[h]);
-          if (at + (lane & 15) <= p_hi && v < INFINITY) most = fmaxf(most, v);
+          if (v < INFINITY) most = fmaxf(most, v);
           t_min = min(t_min, at);
           t_max = max(t_max, at + ATT_BLOCK - 1);
           if ((lane & 15) == 0) s.blk_t[2 * h + q] = at;

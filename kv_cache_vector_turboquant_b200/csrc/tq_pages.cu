@@ -511,6 +511,10 @@ tq_status tq_launch_pages_fork(const tq_page_pool* pools, int n_pools, int64_t n
   const int64_t ints = (int64_t)n_rows * max_blocks + num_blocks;
   const int plan_grid = 1 + (copies ? (int)std::min<int64_t>(sms, ints / PG_SEG + 1) : 0);
   const size_t smem = (size_t)((n_rows + 31) / 32) * 12;
+  // (from 130 700 rows on, with the kernel's static part, above the 48 KB that need no leave)
+  if (smem > 47 * 1024 && cudaFuncSetAttribute(fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               TQ_MAX_PAGE_ROWS / 32 * 12) != cudaSuccess)
+    return TQ_ERR_CUDA;
   fork_plan_kernel<<<plan_grid, PG_PLAN_THREADS, smem, st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
   if (n == 0) return TQ_OK;

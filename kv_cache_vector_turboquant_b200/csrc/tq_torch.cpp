@@ -215,8 +215,8 @@ py::tuple qk_norm_rope(py::handle q_, py::handle k_, py::handle positions_, py::
     ko = tensor(py::object(out[1]), "out k");
     check_shape(qo, "out q", {ScalarType::Half}, {T, hq, d});
     check_shape(ko, "out k", {ScalarType::Half}, {T, hkv, d});
-    apart("out q", qo, {&k, &ko}, &q);
-    apart("out k", ko, {&q, &qo}, &k);
+    apart("out q", qo, {&k, &ko, &positions, &inv_freq, &w[0], &w[1]}, &q);
+    apart("out k", ko, {&q, &qo, &positions, &inv_freq, &w[0], &w[1]}, &k);
   }
   const int dev = one_device({{"q", &q}, {"k", &k}, {"positions", &positions}, {"inv_freq", &inv_freq},
                               {"q_weight", &w[0]}, {"k_weight", &w[1]}, {"out q", &qo}, {"out k", &ko}});
@@ -282,6 +282,8 @@ Tensor attend_window(py::handle q_, uintptr_t k_codec, uintptr_t v_codec, py::ha
   check_numel(lens, "context_lens", {ScalarType::Int}, B);
   if (out.defined()) check_shape(out, "out", {ScalarType::Half}, {T, hq, d});
   if (workspace.defined()) check(workspace, "workspace", {ScalarType::Byte});
+  if (out.defined()) apart("out", out, {&kc, &kn, &vc, &vn, &table, &lens, &offsets, &workspace}, &q);
+  if (workspace.defined()) apart("workspace", workspace, {&q, &kc, &kn, &vc, &vn, &table, &lens, &offsets}, nullptr);
   const int dev = one_device({{"q", &q}, {"q_offsets", &offsets}, {"out", &out}, {"workspace", &workspace},
                               {k_name, &kc}, {v_name, &vc}, {"k_norms", &kn}, {"v_norms", &vn},
                               {"block_tables", &table}, {"context_lens", &lens}});

@@ -91,6 +91,24 @@ def test_fork(K, rows, mb, nb, live, n, layers, hkv, pk, pv, inplace):
     assert K.tq_device_error()[1] == (K.TQ_DEVERR_POOL_FULL if full else 0)
 
 
+def test_fork_of_the_largest_table(K):
+    """As many rows as a call takes, forks at both ends of the table."""
+    rows, nb = K.TQ_MAX_PAGE_ROWS, 40
+    table, lens, refs = [[-1] for _ in range(rows)], [0] * rows, [0] * nb
+    for r, page, length in ((0, 7, 5), (1, 3, 16), (rows - 2, 30, 9)):
+        table[r], lens[r], refs[page] = [page], length, 1
+    parents, children = [0, 1, rows - 2, 0], [rows - 1, rows // 2, 2, rows - 3]
+    pools = _pools(nb, 1, 1, 16, 16, 3)
+    rt, rl, rr, moves, _, _ = R.fork(table, lens, refs, parents, children)
+    expect = _moved(pools, moves)
+    K.tq_device_error()
+    got = K.TQPagePools(pools).fork(_i32(table), _i32(lens), _i32(refs), _i32(parents), _i32(children))
+    for a, b in zip(got, (rt, rl, rr)):
+        assert torch.equal(a, _i32(b))
+    assert all(torch.equal(a, b) for a, b in zip(pools, expect))
+    assert K.tq_device_error() == (K.TQ_OK, 0)
+
+
 def test_no_forks(K):
     """An empty list copies the tables, or does nothing in place."""
     rng = random.Random(5)

@@ -235,6 +235,44 @@ def test_non_finite_norms_where_no_query_looks(K):
     assert torch.equal(ref[1], got[1]) and torch.equal(ref[0, :4], got[0, :4]) and got[0, 4:].isnan().all()
 
 
+@pytest.mark.parametrize("d,n", [(128, 1), (64, 5), (128, 48), (256, 48), (128, 400)])
+@pytest.mark.parametrize("big", [1e30, 3e38])
+def test_huge_norms_where_no_query_looks(K, d, n, big):
+    """Finite norms of any size at positions that no query sees, in blocks that
+    some do: the results are those of the same cache with zeros there."""
+    S, hq, hkv, window, sinks = 700, 4, 2, 43, 3
+    L = S - 5
+    kc, kp, kn = _cache(K, (1, S, hkv), d, 4, 1)
+    vc, vp, vn = _cache(K, (1, S, hkv), d, 2, 2)
+    q = torch.randn(n, hq, d, device="cuda").half()
+    args = (torch.tensor([L], dtype=torch.int32, device="cuda"), window, sinks,
+            torch.tensor([0, n], dtype=torch.int32, device="cuda"), n)
+    got = []
+    for hidden in (0.0, big):
+        for x in (kn, vn):
+            x[:, sinks:L - n - window + 1] = hidden
+            x[:, L:] = hidden
+        got.append(K.attend_window(q, kc, vc, kp, kn, vp, vn, *args))
+    assert got[0].abs().max() > 0 and torch.equal(*got)
+
+
+def test_a_huge_norm_leaves_earlier_row_tiles_as_they_were(K):
+    """The last token's value norm lies in a block that rows of the first row
+    tile (256 rows: tokens 0 to 127) see up to the position before it."""
+    d, S, hq, hkv, n = 128, 640, 4, 2, 136
+    kc, kp, kn = _cache(K, (1, S, hkv), d, 4, 1)
+    vc, vp, vn = _cache(K, (1, S, hkv), d, 2, 2)
+    vn *= 1e-3
+    q = torch.randn(n, hq, d, device="cuda").half()
+    args = (torch.tensor([S], dtype=torch.int32, device="cuda"), None, 0,
+            torch.tensor([0, n], dtype=torch.int32, device="cuda"), n)
+    ref = K.attend_window(q, kc, vc, kp, kn, vp, vn, *args)
+    vn[0, -1] = 3e38
+    got = K.attend_window(q, kc, vc, kp, kn, vp, vn, *args)
+    assert ref.abs().max() > 0 and torch.equal(got[:128], ref[:128])
+    assert not torch.equal(got[-1], ref[-1])
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("n", [4, 64])
 def test_non_finite_norms_reach_the_rows_that_see_them(K, n, bad):

@@ -50,6 +50,7 @@ def test_norm_rope_refusals(K):
     _raises(lambda: f_(slab[:2560].view(5, 4, 128), k, pos, f, out=(slab[8:].view(5, 4, 128), same)), "shares memory")
     _raises(lambda: f_(q.bfloat16(), k.bfloat16(), pos, f, out=(q, k)), "CUDA")
     _raises(lambda: f_(q, k, pos, f, out=(q, k)), "CUDA")  # in place is fine
+    _raises(lambda: f_(q, k, pos, f, out=(q, same), k_weight=same.view(-1)[:128]), "shares memory")
     wide = torch.zeros(5, 4, 132, dtype=torch.float16)[..., :128]
     _raises(lambda: f_(wide, k, pos, f), "strides")
     off = torch.zeros(5 * 4 * 128 + 1, dtype=torch.float16)[1:].view(5, 4, 128)
@@ -106,6 +107,14 @@ def test_window_refusals(K):
     _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, q_offsets=off[:2], max_q=1), "q_offsets: 3")
     _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, out=q.float()), "out: dtype")
     _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, workspace=kn), "workspace: dtype")
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, out=q), "CUDA")  # in place is fine
+    slab = torch.zeros(q.numel() + 128, dtype=torch.float16)
+    part = slab[:q.numel()].view(q.shape)
+    _raises(lambda: f(part, kc, vc, kp, kn, vp, vn, ctx, out=slab[128:].view(q.shape)), "out: shares memory")
+    ws = slab.view(torch.uint8)
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, out=part, workspace=ws), "out: shares memory")
+    _raises(lambda: f(part, kc, vc, kp, kn, vp, vn, ctx, workspace=ws), "workspace: shares memory")
+    _raises(lambda: f(q, kc, vc, kp, kn, vp, vn, ctx, workspace=kp.view(-1)[:64]), "workspace: shares memory")
     pool = [t.reshape(B * S // 16, 16, *t.shape[2:]) for t in (kp, kn, vp, vn)]
     bt = torch.zeros(B, S // 16, dtype=torch.int32)
     p = K.attend_window_paged
