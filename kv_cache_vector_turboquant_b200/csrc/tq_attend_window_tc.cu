@@ -7,16 +7,18 @@
 // A CTA takes MT tiles of 128 query rows (row = token x query head of the
 // group) of one kv head and walks over the 64-position tiles that they see
 // (four 16-position blocks of the list sinks, window). Roles:
-//  * 4 warps turn key codes into level pairs (table lookups as in
-//    tq_attend_window.cu, 16 lane copies) and write them as a K-major,
-//    128-byte-swizzled operand [64 positions x d]; their first warp also puts
-//    the tile's norms and positions into a ring of slots;
+//  * 4 warps turn key codes into fp16 levels and write them as a K-major,
+//    128-byte-swizzled operand [64 positions x d]. Codes of 2 and 4 bits are
+//    looked up by byte permutes (no shared memory, whose ports the products
+//    need: 8 x 5 tokens at 4 bits 67.5 -> 65.9 us against tables), 3-bit codes
+//    in pairs from a table of 16 lane copies;
 //  * 4 warps do the same for the values, transposed, [d x 64 positions]: a
 //    thread takes 8 positions x 8 neighbouring dims, whose codes are one word
 //    per position, and writes dim 8 dg + j to row j d/8 + dg (then the 8
 //    lanes of a store phase hit 8 different bank groups). The accumulator's
 //    columns come out in that order; a Hadamard transform commutes with such
 //    a permutation of index bits, so the final rotation is done in it;
+//  * a spare warp puts the tiles' norms and positions into a ring of slots;
 //  * one warp per row tile issues tcgen05.mma: S = (Q_hi + Q_lo) K^T into
 //    tensor memory, and O += (P_hi + P_lo) V with P read from tensor memory;
 //  * 4 warps per row tile, one row per thread: scores from tensor memory,
@@ -39,12 +41,19 @@
 // 9 other instructions per score and the codes' conversion (about 1000 warp
 // instructions, shared by the row tiles). Measured, 2 x 2048 tokens of 32 query
 // and 8 kv heads of 128 within 4096 + 64 positions, keys 4 and values 2 bits:
-// 603 us, 0.93 PFLOP/s with the remainders counted; a CTA's loop takes
-// about 3700 cycles per 64 positions and its start and end 40 000, and 512
+// 625 us a call, 0.89 PFLOP/s with the remainders counted. A CTA's loop takes
+// about 3700 cycles per 64 positions, of which a softmax warp works 3300 (some
+// 550 instructions at 6 cycles each: 20 warps, a fifth of the wait for
+// instructions; issue slots 54 %, tensor pipe 50 %), so the softmax of a row
+// tile is the bound, not the products; its start takes 12 000 to 16 000 cycles
+// (8 000 of them the rotation of the query rows) and its end 9 000, and 512
 // CTAs leave 148 SMs 3.46 waves. 8 x 5 tokens of 8 query heads per kv head over
-// 8000 positions: 66 us.
+// 8000 positions, 4 bits: 66 us (two softmax groups and the value conversion,
+// 2000 cycles a tile, both take about 4000 cycles per two tiles). Loading codes
+// one more tile ahead changes nothing.
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "tq_attend_window.cuh"
 #include "tq_umma.cuh"
@@ -81,8 +90,9 @@ struct TwCfg {
   static_assert(MT * R_SM + 2 * R_CV + R_MMA <= (MT + 3) * (MT == 2 ? 96 : 128), "register shares");
   static constexpr int Q_PART = D * 256;         // [128 rows x d] fp16
   static constexpr int KV = D * TW_TP * 2;       // [64 x d] fp16
-  static constexpr int K_TAB = KB == 2 ? 0 : (1 << (2 * KB)) * 64;
-  static constexpr int V_TAB = VB == 2 || KB == VB ? 0 : (1 << (2 * VB)) * 64;
+  // tables of the 3-bit codes (one serves both); 2 and 4 bits go by byte permutes
+  static constexpr int K_TAB = KB == 3 ? 64 * 64 : 0;
+  static constexpr int V_TAB = VB == 3 && KB != 3 ? 64 * 64 : 0;
   static constexpr int Q0 = 0;
   static constexpr int K0 = Q0 + 2 * MT * Q_PART;
   static constexpr int V0 = K0 + NBUF * KV;
@@ -115,6 +125,36 @@ TQ_DEV void wht64(float (&x)[64]) {
 // a byte permute of the four levels in two words, code c taking bytes 2c, 2c + 1.
 TQ_DEV uint32_t tw_levels2(uint32_t x, uint32_t lo, uint32_t hi) {
   return __byte_perm(lo, hi, (x & 0x0303u) * 0x22u + 0x1010u);
+}
+
+// The same for 4-bit codes, eight in a word. The codebook is symmetric (level
+// 15 - c is minus level c), so the byte permutes look up the bytes of the eight
+// positive levels by c - 8 or 7 - c, and the sign is put into the high bytes.
+struct TwLevels16 {
+  uint32_t l0, l1, h0, h1;  // low and high bytes of levels 8 ... 15
+};
+TQ_DEV TwLevels16 tw_table16(const uint16_t* lev) {
+  TwLevels16 t;
+  const uint32_t a = lev[8] | (uint32_t)lev[9] << 16, b = lev[10] | (uint32_t)lev[11] << 16;
+  const uint32_t c = lev[12] | (uint32_t)lev[13] << 16, d = lev[14] | (uint32_t)lev[15] << 16;
+  t.l0 = __byte_perm(a, b, 0x6420);
+  t.h0 = __byte_perm(a, b, 0x7531);
+  t.l1 = __byte_perm(c, d, 0x6420);
+  t.h1 = __byte_perm(c, d, 0x7531);
+  return t;
+}
+TQ_DEV void tw_levels8(uint32_t x, const TwLevels16& t, uint32_t (&w)[4]) {
+  const uint32_t neg = ~x & 0x88888888u;                          // bit 3 of the negative levels' codes
+  const uint32_t m = (x ^ (neg - (neg >> 3))) & 0x77777777u;      // c - 8 or 7 - c
+  const uint32_t se = (neg << 4) & 0x80808080u, so = neg & 0x80808080u;  // signs of the even, the odd codes
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t sel = k ? m >> 16 : m;
+    const uint32_t lo = __byte_perm(t.l0, t.l1, sel);
+    const uint32_t hi = __byte_perm(t.h0, t.h1, sel) | __byte_perm(se, so, k ? 0x7362 : 0x5140);
+    w[2 * k] = __byte_perm(lo, hi, 0x5140);
+    w[2 * k + 1] = __byte_perm(lo, hi, 0x7362);
+  }
 }
 
 // Bounded wait for phase `parity` of a barrier. Twenty warps polling as
@@ -293,6 +333,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
       [[maybe_unused]] const uint32_t lut = base + C::T0 + (lane & 15) * 4u;
       [[maybe_unused]] const uint32_t k_lo = a.k_lev[0] | (uint32_t)a.k_lev[1] << 16,
                                       k_hi = a.k_lev[2] | (uint32_t)a.k_lev[3] << 16;
+      [[maybe_unused]] const TwLevels16 k_t = tw_table16(a.k_lev);
       uint32_t cw[HW];
       int next = 0;  // table entry of the tile after the loaded one
       auto fetch = [&](int i) {
@@ -325,6 +366,8 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
             w[1] = __byte_perm(p[2], p[3], 0x5410);
             w[2] = __byte_perm(p[0], p[1], 0x7632);
             w[3] = __byte_perm(p[2], p[3], 0x7632);
+          } else if constexpr (KB == 4) {
+            tw_levels8(cw[c], k_t, w);
           } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[k] = lds32(aw_bits<2 * KB>(cw, (4 * c + k) * 2 * KB) * 64u + lut);
@@ -345,6 +388,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
       [[maybe_unused]] const uint32_t lut = base + C::T0 + C::K_TAB * (KB == VB ? 0 : 1) + (lane & 15) * 4u;
       [[maybe_unused]] const uint32_t v_lo = a.v_lev[0] | (uint32_t)a.v_lev[1] << 16,
                                       v_hi = a.v_lev[2] | (uint32_t)a.v_lev[3] << 16;
+      [[maybe_unused]] const TwLevels16 v_t = tw_table16(a.v_lev);
       uint32_t vw[PASS][8];
       int next[PASS];
       auto fetch = [&](int i) {
@@ -391,6 +435,21 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) e[k] = tw_levels2(pair[k] >> (16 * (j >> 2) + 2 * (j & 3)), v_lo, v_hi);
                 *reinterpret_cast<uint4*>(dst + j * DG * 128) = make_uint4(e[0], e[1], e[2], e[3]);
+              }
+            } else if constexpr (VB == 4) {
+              constexpr uint32_t LOWS = 0x0f0f0f0fu;
+#pragma unroll
+              for (int odd = 0; odd < 2; ++odd) {  // dims 8 dg + odd, + 2, + 4, + 6
+                uint32_t e[4][4];                  // of position pair k: its words for the four dims
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {  // codes of two positions side by side, dim by dim
+                  const uint32_t x = vw[q][2 * k], y = vw[q][2 * k + 1];
+                  tw_levels8(odd ? ((x >> 4) & LOWS) | (y & ~LOWS) : (x & LOWS) | ((y << 4) & ~LOWS), v_t, e[k]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  *reinterpret_cast<uint4*>(dst + (2 * j + odd) * DG * 128) =
+                      make_uint4(e[0][j], e[1][j], e[2][j], e[3][j]);
               }
             } else {
 #pragma unroll
@@ -794,15 +853,21 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
         }
       }
       __syncwarp();
-      const int chunks = a.n_split > 1 ? D / 4 : D / 8;  // of 16 bytes, per row
-      uint8_t* to = a.n_split > 1 ? reinterpret_cast<uint8_t*>(a.ws_acc) : reinterpret_cast<uint8_t*>(a.out);
-      const int64_t row_to = a.n_split > 1 ? idx : out_row;
-      for (int e = lane; e < 32 * chunks; e += 32) {
-        const int rr = e / chunks, c = e % chunks;
-        const int64_t at = __shfl_sync(FULL, row_to, rr) * (16 * chunks) + 16 * c;
-        const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * (4 * D) + ((c & ~7) << 4) + (((c ^ rr) & 7) << 4));
-        if (rw0 + rr < rows) *reinterpret_cast<uint4*>(to + at) = w;
-      }
+      auto leave = [&](auto chunks_, uint8_t* to, int64_t row_to) {
+        constexpr int chunks = decltype(chunks_)::value;  // of 16 bytes, per row
+#pragma unroll 8
+        for (int it = 0; it < chunks; ++it) {
+          const int e = it * 32 + lane, rr = e / chunks, c = e % chunks;
+          const int64_t at = __shfl_sync(FULL, row_to, rr) * (16 * chunks) + 16 * c;
+          const uint4 w =
+              *reinterpret_cast<const uint4*>(stage + rr * (4 * D) + ((c & ~7) << 4) + (((c ^ rr) & 7) << 4));
+          if (rw0 + rr < rows) *reinterpret_cast<uint4*>(to + at) = w;
+        }
+      };
+      if (a.n_split > 1)
+        leave(std::integral_constant<int, D / 4>(), reinterpret_cast<uint8_t*>(a.ws_acc), idx);
+      else
+        leave(std::integral_constant<int, D / 8>(), reinterpret_cast<uint8_t*>(a.out), out_row);
     }
   }
   tc_fence_before();
