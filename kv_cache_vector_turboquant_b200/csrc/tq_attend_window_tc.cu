@@ -108,16 +108,19 @@ struct TwCfg {
   static_assert(BYTES <= 232448, "shared memory of a CTA");
 };
 
-// In-register Hadamard transform of 64 values (natural order, no scaling).
-TQ_DEV void wht64(float (&x)[64]) {
+// In-register Hadamard transform of 64 values (natural order, no scaling), two
+// in a register pair: all stages but the first are packed additions.
+TQ_DEV void wht64(f2 (&x)[32]) {
 #pragma unroll
-  for (int h = 1; h < 64; h <<= 1)
+  for (int e = 0; e < 32; ++e) x[e] = make_float2(x[e].x + x[e].y, x[e].x - x[e].y);
 #pragma unroll
-    for (int e = 0; e < 64; ++e)
+  for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
       if ((e & h) == 0) {
-        const float u = x[e], v = x[e + h];
-        x[e] = u + v;
-        x[e + h] = u - v;
+        const f2 u = x[e], v = x[e + h];
+        x[e] = add2(u, v);
+        x[e + h] = sub2(u, v);
       }
 }
 
@@ -624,7 +627,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
     if (row_ok) {
       const uint8_t* src = sm + C::K0 + r_cta * (2 * D);
       const int sw = (r_cta & 7) << 4;
-      float ss = 0.f;
+      f2 s2 = make_float2(0.f, 0.f);
 #pragma unroll 4
       for (int e = 0; e < D / 8; ++e) {
         const uint4 w = *reinterpret_cast<const uint4*>(src + ((e & ~7) << 4) + (((e & 7) << 4) ^ sw));
@@ -632,20 +635,22 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hw[c]));
-          ss = fmaf(f.x, f.x, fmaf(f.y, f.y, ss));
+          s2 = fma2(f, f, s2);
         }
       }
+      const float ss = s2.x + s2.y;
       // no rotated coordinate exceeds sqrt(d) |q|: that bound is put just below 2^15
       const float up = aw_pow2_for<14>(sqrtf(ss * (float)D) * a.q_scale, row_inv);
       const float qs = a.q_scale * up;
 #pragma unroll 1
       for (int hf = 0; hf < D / 64; ++hf) {
-        float x[64];
+        f2 x[32];
 #pragma unroll
-        for (int e = 0; e < 64; ++e) x[e] = 0.f;
+        for (int e = 0; e < 32; ++e) x[e] = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int m = 0; m < D / 64; ++m) {
-          const float sg = (__popc(m & hf) & 1) ? -1.f : 1.f;
+          const float sg1 = (__popc(m & hf) & 1) ? -1.f : 1.f;
+          const f2 sg = make_float2(sg1, sg1);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const uint4 w = *reinterpret_cast<const uint4*>(src + (m << 7) + ((e << 4) ^ sw));
@@ -654,22 +659,21 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
             for (int c = 0; c < 4; ++c) {
               const uint32_t s = hw[c] ^ a.k_sign_h2[32 * m + 4 * e + c];
               const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&s));
-              x[8 * e + 2 * c] = fmaf(sg, f.x, x[8 * e + 2 * c]);
-              x[8 * e + 2 * c + 1] = fmaf(sg, f.y, x[8 * e + 2 * c + 1]);
+              x[4 * e + c] = fma2(sg, f, x[4 * e + c]);
             }
           }
         }
-      wht64(x);
+        wht64(x);
         uint8_t* dst = sm + C::Q0 + 2 * mt * C::Q_PART + hf * 16384 + r_tile * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float u = x[8 * c + 2 * k] * qs, v = x[8 * c + 2 * k + 1] * qs;
-            hi[k] = pack_half2(u, v);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
-            lo[k] = pack_half2(u - f.x, v - f.y);
+            const f2 u = mul2(x[4 * c + k], make_float2(qs, qs));
+            hi[k] = pack_half2(u.x, u.y);
+            const f2 r = sub2(u, __half22float2(*reinterpret_cast<const __half2*>(&hi[k])));
+            lo[k] = pack_half2(r.x, r.y);
           }
           const int off = (c ^ (r_tile & 7)) << 4;
           *reinterpret_cast<uint4*>(dst + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -818,13 +822,14 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
       uint8_t* stage = sm + C::Q0 + 2 * mt * C::Q_PART + 32 * (warp & 3) * (4 * D);
 #pragma unroll 1
       for (int hf = 0; hf < D / 64; ++hf) {
-        float x[64];
+        f2 x[32];
 #pragma unroll
-        for (int e = 0; e < 64; ++e) x[e] = 0.f;
+        for (int e = 0; e < 32; ++e) x[e] = make_float2(0.f, 0.f);
         if (n > 0) {
 #pragma unroll 1
           for (int m = a.n_split > 1 ? hf : 0; m < (a.n_split > 1 ? hf + 1 : D / 64); ++m) {
-            const float sg = a.n_split > 1 || !(__popc(m & hf) & 1) ? 1.f : -1.f;
+            const float sg1 = a.n_split > 1 || !(__popc(m & hf) & 1) ? 1.f : -1.f;
+            const f2 sg = make_float2(sg1, sg1);
 #pragma unroll
             for (int c0 = 0; c0 < 64; c0 += 16) {
               uint32_t u[16];
@@ -832,19 +837,22 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
               tmem_wait_ld();
               tmem_regs_after_wait(u);
 #pragma unroll
-              for (int c = 0; c < 16; ++c) x[c0 + c] = fmaf(sg, __uint_as_float(u[c]), x[c0 + c]);
+              for (int c = 0; c < 16; c += 2)
+                x[(c0 + c) / 2] =
+                    fma2(sg, make_float2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), x[(c0 + c) / 2]);
             }
           }
         }
         if (a.n_split == 1) wht64(x);
         // column 64 hf + e is dim 8 (e % DG) + JN hf + e / DG: JN neighbouring dims per group
         constexpr int DG = D / 8, JN = 64 / DG;
+        auto at_col = [&](int e) { return e & 1 ? x[e / 2].y : x[e / 2].x; };
 #pragma unroll
         for (int dg = 0; dg < DG; ++dg) {
           const int dim = 8 * dg + JN * hf;
 #pragma unroll
           for (int j = 0; j < JN; j += 2) {
-            const float u = x[j * DG + dg] * scale, v = x[(j + 1) * DG + dg] * scale;
+            const float u = at_col(j * DG + dg) * scale, v = at_col((j + 1) * DG + dg) * scale;
             const int at = (a.n_split > 1 ? 4 : 2) * (dim + j);
             uint8_t* dst = stage + lane * (4 * D) + (at & ~112) + ((at ^ (lane << 4)) & 112);
             if (a.n_split > 1) *reinterpret_cast<float2*>(dst) = make_float2(u, v);
