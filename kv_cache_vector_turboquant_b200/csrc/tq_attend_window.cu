@@ -726,11 +726,25 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_consta
     dst[e / 2] = pack_half2(x[e] * inv, x[e + 1] * inv) ^ a.v_sign_h2[(lane * E + e) / 2];
 }
 
-// Query rows per kv head from which the tensor-memory kernel takes a call: it
-// costs the same up to 256 rows (128 at d = 256), this one in proportion.
-// Measured, 8 sequences of up to 8000 positions (this kernel / that one): 16
-// rows 66 / 114 us, 40 rows (4 kv heads) 81 / 75, 64 rows 220 / 119.
-constexpr int64_t AW_TC_ROWS = 40;
+// Which kernel takes a call. This one costs in proportion to the query rows per
+// kv head, the tensor-memory kernel the same up to 128 (d = 256) or 256 rows,
+// but more to start; so that one takes 64 rows and more, this one fewer than 40
+// (32 at d = 256), and between them the estimates below decide (us; `seen`
+// positions at most). Measured, this kernel / that one, keys 4 and values 2 bits:
+//   d = 128, 8 sequences x 4 kv heads x 8000: 32 rows 56 / 62, 40 rows 68 / 63, 64 rows 105 / 63
+//            32 x 8 x 1000: 40 rows 60 / 81, 48 rows 97 / 81;  32 x 8 x 2000: 106 / 122, 169 / 123
+//            8 x 8 x 2000: 40 rows 46 / 39;  1 x 8 x 300: 48 rows 15 / 23;  1 x 8 x 1000: 48 rows 18 / 25
+//   d = 64 (3 / 3 bits), 32 x 8 x 1000: 40 rows 60 / 64, 48 rows 97 / 64;  8 x 8 x 4000: 40 rows 58 / 56
+//   d = 256, 8 x 4 x 4000: 24 rows 53 / 66, 32 rows 72 / 65;  2 x 4 x 4000: 32 rows 33 / 37, 48 rows 41 / 39
+static bool window_takes_tc(int64_t rows, int64_t units, int d, int64_t seen) {
+  if (rows < (d == 256 ? 32 : 40)) return false;
+  if (rows >= 64) return true;
+  const double here = 12.0 + (d == 64 ? 3.7e-5 : d == 128 ? 4.6e-5 : 1.2e-4) * (double)(units * ((rows + 7) / 8)) * seen;
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(148 / units, (seen + 255) / 256));
+  const int64_t waves = (units * splits + 147) / 148;
+  const double there = 6.0 + waves * (12.0 + (d == 64 ? 0.019 : d == 128 ? 0.023 : 0.05) * seen / splits);
+  return there < here;
+}
 // With at most 128 of them, and no more than one row tile of head_dim 64 or 128
 // in use, the tensor-memory kernel's two row tiles hold the same rows and take
 // alternate tiles of positions, each as a split of its own, from this many
@@ -749,15 +763,15 @@ struct WindowPlan {
 };
 static WindowPlan window_plan(int B, int hq, int hkv, int max_q, int d, int64_t s_max, int64_t window, int64_t sinks) {
   WindowPlan p{};
-  p.tc = (int64_t)max_q * (hq / hkv) >= AW_TC_ROWS;
-  const bool tc = p.tc;
   const int64_t rows = (int64_t)max_q * (hq / hkv);
-  const int64_t rt = tc ? tq_window_tc_rows(d) : rows > 4 && d <= 128 ? 8 : 4;
-  const int64_t tiles = (rows + rt - 1) / rt;
-  const int64_t units = (int64_t)B * hkv * tiles;
   int64_t seen = s_max;
   if (window > 0)  // (s_max is below 2^31; larger limits are none)
     seen = std::min(seen, std::min<int64_t>(window, INT_MAX) + std::min<int64_t>(sinks, INT_MAX) + max_q + 2 * ATT_BLOCK);
+  p.tc = window_takes_tc(rows, (int64_t)B * hkv, d, seen);
+  const bool tc = p.tc;
+  const int64_t rt = tc ? tq_window_tc_rows(d) : rows > 4 && d <= 128 ? 8 : 4;
+  const int64_t tiles = (rows + rt - 1) / rt;
+  const int64_t units = (int64_t)B * hkv * tiles;
   const int64_t steps = tc ? (seen + 255) / 256 : (seen + AW_TILE - 1) / AW_TILE;
   const int64_t slots = tc ? 148 : 148 * (d * rt <= 512 ? 16 : 8);
   p.n_split = (int)std::max<int64_t>(1, std::min<int64_t>(slots / units, steps));

@@ -201,6 +201,25 @@ def test_many_rows_with_empty_and_short_contexts(K, d):
     assert torch.all(out[off[2]:off[2] + 47] == 0) and torch.all(out[off[3]:off[4]] == 0)
 
 
+@pytest.mark.parametrize("d,n,g", [(128, 6, 8), (64, 9, 5), (256, 4, 8), (128, 5, 8)])
+@pytest.mark.parametrize("B", [1, 64])
+def test_between_the_kernels(K, d, n, g, B):
+    """32 to 63 query rows per kv head, where the sizes choose the kernel: one
+    sequence and many of the same one."""
+    S, L, hkv = 1104, 1090, 2
+    kc, kp, kn = _cache(K, (1, S, hkv), d, 4, 1)
+    vc, vp, vn = _cache(K, (1, S, hkv), d, 2, 2)
+    q = torch.randn(n, hkv * g, d, device="cuda").half()
+    caches = [x.expand(B, *x.shape[1:]).contiguous() for x in (kp, kn, vp, vn)]
+    o = K.attend_window(q.repeat(B, 1, 1), kc, vc, *caches, torch.full((B,), L, dtype=torch.int32, device="cuda"),
+                        q_offsets=n * torch.arange(B + 1, dtype=torch.int32, device="cuda"), max_q=n)
+    kk, vv = R.decode_rows(kp[0], kn[0], 4, d), R.decode_rows(vp[0], vn[0], 2, d)
+    ref, tol = R.attend(q, kk, vv, L, None, 0, 4, 2)
+    o = o.view(B, n, hkv * g, d)
+    _check(o[0], ref, tol)
+    assert torch.equal(o, o[:1].expand_as(o))
+
+
 @pytest.mark.parametrize("n", [1, 48])
 def test_output_in_place_of_the_queries(K, n):
     d, S, hq, hkv = 128, 700, 8, 2
