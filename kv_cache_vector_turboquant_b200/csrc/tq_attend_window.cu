@@ -745,10 +745,11 @@ static bool window_takes_tc(int64_t rows, int64_t units, int d, int64_t seen) {
   const double there = 6.0 + waves * (12.0 + (d == 64 ? 0.019 : d == 128 ? 0.023 : 0.05) * seen / splits);
   return there < here;
 }
-// With at most 128 of them, and no more than one row tile of head_dim 64 or 128
+
+// With at most 128 query rows per kv head, so one row tile of head_dim 64 or 128
 // in use, the tensor-memory kernel's two row tiles hold the same rows and take
 // alternate tiles of positions, each as a split of its own, from this many
-// positions on. Measured, d = 128 (one row tile / halves): 8 sequences of 8000
+// positions on. Measured when this was built, d = 128 (one row tile / halves): 8 sequences of 8000
 // positions 78 / 68 us, 32 sequences of 2048 135 / 130, of 1024 86 / 86, of
 // 512 63 / 68 (twice the partial results to merge).
 constexpr int64_t AW_HALVES = 1024;
