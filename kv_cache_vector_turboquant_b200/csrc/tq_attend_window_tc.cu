@@ -804,8 +804,12 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
       mbar_arrive(p_full + 16 * mt + 8 * (j & 1));
     }
     // ---- results
-    if (ok && n > 0) {
-      ok = __all_sync(FULL, tw_wait(mma_end + 8 * mt, 0, TW_TRIES));  // every product is done
+    if (ok) {
+      // every product is done; and, also where there is none (no row of the
+      // CTA sees a position), the tile's other softmax warps have written
+      // their query rows into the space that the results below go to: the
+      // issuer signals after q_full
+      ok = __all_sync(FULL, tw_wait(mma_end + 8 * mt, 0, TW_TRIES));
       if (!ok && lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
       tc_fence_after();
     }

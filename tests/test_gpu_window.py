@@ -201,6 +201,40 @@ def test_many_rows_with_empty_and_short_contexts(K, d):
     assert torch.all(out[off[2]:off[2] + 47] == 0) and torch.all(out[off[3]:off[4]] == 0)
 
 
+@pytest.mark.parametrize("rows", [128, 256])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_whole_row_tiles_that_see_nothing(K, d, rows):
+    """Unsplit calls whose row tiles are full and see no position: contexts of
+    0 and tokens before position 0. Every element is zero, every time, and the
+    tokens behind them are those of a call of their own."""
+    S, hq, hkv, kb, vb, seen = 40, 2, 1, 4, 2, 9
+    n = rows // 2
+    kc, kp, kn = _cache(K, (1, S, hkv), d, kb, 1)
+    vc, vp, vn = _cache(K, (1, S, hkv), d, vb, 2)
+    B = 148
+    lens = [0 if b % 3 else seen for b in range(B)]  # sequences of 2 n tokens: the first n see nothing
+    caches = [x.expand(B, *x.shape[1:]).contiguous() for x in (kp, kn, vp, vn)]
+    assert K.tq_attend_window_workspace_bytes(2 * n * B, B, 2 * n, hq, hkv, d, S, 0, 0) == 0
+    q = 10 * torch.randn(2 * n, hq, d, device="cuda").half()
+    some = K.attend_window(q[-seen:].contiguous(), kc, vc, kp, kn, vp, vn,
+                           torch.tensor([seen], dtype=torch.int32, device="cuda"),
+                           q_offsets=torch.tensor([0, seen], dtype=torch.int32, device="cuda"), max_q=seen)
+    kk, vv = R.decode_rows(kp[0, :seen], kn[0, :seen], kb, d), R.decode_rows(vp[0, :seen], vn[0, :seen], vb, d)
+    ref, tol = R.attend(q[-seen:], kk, vv, seen, None, 0, kb, vb)
+    _check(some, ref, tol)
+    args = (torch.tensor(lens, dtype=torch.int32, device="cuda"), None, 0,
+            2 * n * torch.arange(B + 1, dtype=torch.int32, device="cuda"), 2 * n)
+    for _ in range(20):
+        out = torch.full((B * 2 * n, hq, d), 7.0, dtype=torch.float16, device="cuda")
+        K.attend_window(q.repeat(B, 1, 1), kc, vc, *caches, *args, out=out)
+        o = out.view(B, 2 * n, hq, d)
+        assert torch.all(o[:, :-seen] == 0)
+        assert torch.all(o[1::3] == 0) and torch.all(o[2::3] == 0)
+        _check(o[0, -seen:], ref, tol)
+        assert torch.equal(o[::3], o[:1].expand_as(o[::3]))
+    assert K.tq_device_error() == (K.TQ_OK, 0)
+
+
 @pytest.mark.parametrize("d,n,g", [(128, 6, 8), (64, 9, 5), (256, 4, 8), (128, 5, 8)])
 @pytest.mark.parametrize("B", [1, 64])
 def test_between_the_kernels(K, d, n, g, B):
