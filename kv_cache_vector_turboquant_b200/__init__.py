@@ -465,8 +465,9 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
     scaling: None; "linear" (every frequency divided by factor); "ntk" (the
     base grows so that the lowest frequency is divided by factor and the
     highest kept); "yarn" (frequencies of more than beta_fast turns within
-    original_len kept, of fewer than beta_slow divided by factor, a ramp
-    between, and rope_scale 1 + 0.1 ln(factor)).
+    original_len kept, of fewer than beta_slow divided by factor, between them
+    a linear ramp over the index, whose ends are rounded outward to whole
+    indices within 0 ... rot_dim - 1, and rope_scale 1 + 0.1 ln(factor)).
     """
     import math
 
@@ -485,11 +486,12 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
         f = f / factor
     elif scaling == "yarn":
         _require(beta_fast > beta_slow > 0, "beta_fast > beta_slow > 0")
-        turns = original_len * f / (2 * math.pi)
-        # the ramp runs over the index i, between those at which a frequency turns beta_fast and beta_slow times
+        # the ramp runs over the index i, between those at which a frequency turns beta_fast and beta_slow times;
+        # its upper end may lie behind the last index (every frequency turns more than beta_slow times)
         at = [rot_dim * math.log(original_len / (b * 2 * math.pi)) / (2 * math.log(base)) for b in (beta_fast, beta_slow)]
-        lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot_dim // 2 - 1)
-        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        hi = min(math.ceil(at[1]), rot_dim - 1)
+        lo = min(max(math.floor(at[0]), 0), hi - 1)
+        ramp = ((i - lo) / (hi - lo)).clamp(0, 1)
         f = f * (1 - ramp) + f / factor * ramp
         scale = 0.1 * math.log(factor) + 1.0
     return f.to(device), scale

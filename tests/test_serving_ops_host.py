@@ -79,6 +79,42 @@ def test_frequencies(K):
             bad()
 
 
+@pytest.mark.parametrize("rot,base,length,factor,fast,slow", [
+    (64, 1e4, 4096, 4.0, 32.0, 1.0), (128, 1e4, 32768, 4.0, 32.0, 1.0), (128, 5e5, 8192, 8.0, 32.0, 1.0),
+    # the slowest frequency turns more than beta_slow times
+    (128, 1e4, 131072, 4.0, 32.0, 1.0), (64, 1e4, 65536, 8.0, 32.0, 1.0), (20, 1e4, 32768, 8.0, 32.0, 1.0),
+    (64, 1e4, 1 << 20, 2.0, 64.0, 2.0), (2, 1e4, 4096, 2.0, 32.0, 1.0),
+    # more than beta_fast times, and none of them: all kept
+    (64, 100.0, 1 << 20, 4.0, 32.0, 1.0),
+    # the fastest one turns less often than beta_fast, less often than beta_slow
+    (64, 1e4, 100, 4.0, 32.0, 1.0), (64, 1e4, 3, 4.0, 32.0, 1.0), (64, 1e4, 1, 4.0, 32.0, 1.0)])
+def test_yarn_follows_the_published_rule(K, rot, base, length, factor, fast, slow):
+    """The ramp between the indices at which a frequency turns `fast` and
+    `slow` times within `length`, rounded outward and kept within
+    [0, rot - 1], written out for every index."""
+    got, s = K.rope_frequencies(rot, base, "yarn", factor, length, fast, slow, device="cpu")
+    assert math.isclose(s, 1 + 0.1 * math.log(factor))
+
+    def index(turns):  # base^(-2 i / rot) length = 2 pi turns
+        return rot / 2 * math.log(length / (2 * math.pi * turns), base)
+
+    first, last = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), rot - 1)
+    for i in range(rot // 2):
+        f = base ** (-2 * i / rot)
+        if length * f / (2 * math.pi) < slow and i >= index(slow) + 1:
+            expect = f / factor
+        elif length * f / (2 * math.pi) > fast and i <= first:
+            expect = f
+        elif last <= 0:  # even the fastest frequency turns less than `slow` times
+            expect = f / factor
+        else:
+            share = min(max((i - first) / (last - first), 0.0), 1.0) if last > first else 0.0
+            expect = f / factor * share + f * (1 - share)
+        assert math.isclose(got[i].item(), expect, rel_tol=1e-12), i
+        if length * f / (2 * math.pi) > fast:
+            assert math.isclose(got[i].item(), f, rel_tol=1e-12)
+
+
 def test_window_refusals(K):
     kc, vc = K.TurboQuant(128, 4), K.TurboQuant(128, 2)
     B, S, hkv, hq = 2, 32, 2, 8
