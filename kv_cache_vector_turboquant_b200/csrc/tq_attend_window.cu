@@ -36,9 +36,13 @@
 // times a common factor that puts them within 2^-14 of fp16 values (host,
 // lev_f16), the rotated query as value + remainder (22 bits) scaled by a power
 // of two per row, and weight x norm as value + remainder, scaled by a power of
-// two that follows the largest value norm seen, so norms of any size neither
-// overflow nor vanish. The maximum that the weights refer to moves only when
-// it grows by more than 2^8 (exact: sum and accumulator share it).
+// two that follows the largest value norm that a row of the warp sees (up to
+// 2^14: nothing overflows). A row whose own products are much smaller takes a
+// lower reference for its weights (aw_reference), so each product is off by
+// 2^-22 of itself or 2^-26 of the row's largest, whatever other rows see, for
+// norms within 2^90 of the largest. The reference moves only when a score
+// exceeds it by more than 2^8 or the row's products are small (exact: sum and
+// accumulator share it).
 //
 // Bound: (P_K + P_V + 8) bytes per visible position and kv head, against about
 // 680 warp instructions and 200 shared-memory wavefronts per 32 positions and
@@ -372,10 +376,13 @@ __global__ void __launch_bounds__(AwCfg<D, KB, VB, NT>::WARPS * 32, 1)
 
   const uint32_t lut_k = table + (KB == 2 ? (lane & 15) * 8u : lane * 4u);
   const uint32_t lut_v = table + 128u + (VB == 2 ? (lane & 15) * 8u : lane * 4u);
-  float m_ref[NT], l_run[NT], acc[NT][NB][4];
+  // w_low: a lower bound of the largest |weight x norm| of the row so far
+  // (infinite before the row's first position: no reason to move)
+  float m_ref[NT], w_low[NT], l_run[NT], acc[NT][NB][4];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     m_ref[j] = -INFINITY;
+    w_low[j] = INFINITY;
     l_run[j] = 0.f;
 #pragma unroll
     for (int i = 0; i < NB; ++i)
@@ -498,14 +505,26 @@ __global__ void __launch_bounds__(AwCfg<D, KB, VB, NT>::WARPS * 32, 1)
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const float mx = warp_max8(fmaxf(fmaxf(sc[j][0][0], sc[j][0][1]), fmaxf(sc[j][1][0], sc[j][1][1])));
-      const bool move = mx > m_ref[j] + 8.0f;  // from -inf by any score
+      w_low[j] *= fix_all;
+      const bool move = mx > m_ref[j] + 8.0f || w_low[j] < AW_SMALL;  // from -inf by any score
       if (__any_sync(0xffffffffu, move || fix_all != 1.f)) {
         float fix = fix_all;
+        const float top = fmaxf(m_ref[j], mx);
+        float most = 0.f;  // of this tile, at `top` (NaN, from masked norms, left out)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) most = fmaxf(most, aw_exp2(sc[j][h][r] - top) * fabsf(nv[h][r] * v_up));
+        most = warp_max8(most);
+        const float sum = warp_max8(l_run[j]);  // within a factor of 8
         if (move) {
-          const float f = aw_exp2(m_ref[j] - mx);
+          const float old = aw_exp2(m_ref[j] - top);
+          most = fmaxf(most, w_low[j] * old);  // (inf * 0 = NaN is left out)
+          const float ref = aw_reference(top, sum * old, most), f = aw_exp2(m_ref[j] - ref);
           l_run[j] *= f;
           fix *= f;
-          m_ref[j] = mx;
+          m_ref[j] = ref;
+          w_low[j] = most;
         }
         // (the accumulator's columns 2 tq, 2 tq + 1 belong to this same row)
 #pragma unroll

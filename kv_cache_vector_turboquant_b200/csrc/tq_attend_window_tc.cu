@@ -23,10 +23,10 @@
 //    tensor memory, and O += (P_hi + P_lo) V with P read from tensor memory;
 //  * 4 warps per row tile, one row per thread: scores from tensor memory,
 //    times the key norm, running maximum, weights times value norms as fp16
-//    value + remainder back to tensor memory, over the scores. The maximum
-//    that the weights refer to moves only when it grows by more than 2^8
-//    (exact: sum and accumulator share it), so the accumulator is rescaled
-//    rarely.
+//    value + remainder back to tensor memory, over the scores. The reference
+//    of the weights moves only when a score exceeds it by more than 2^8 or the
+//    row's products with the norms are small (aw_reference; exact: sum and
+//    accumulator share it), so the accumulator is rescaled rarely.
 // Scores are double-buffered: the next tile's S is computed while the
 // softmax works on the current one. Calls whose rows fit one row tile may have
 // it twice (`halves`): both hold the same rows, and each walks over every
@@ -73,7 +73,8 @@ struct TwSlot {
   int t_min, t_max;  // first and last position
   float v_up, v_inv; // this tile's power of two and its inverse
   uint32_t odd[2];   // positions whose value norm is infinite or NaN (0 in nv)
-  int pad[2];
+  float nv_min;      // smallest finite |nv| that a row sees
+  int pad;
 };
 
 template <int D, int KB, int VB>
@@ -221,6 +222,26 @@ TQ_DEV uint32_t tw_visible16(int t0, int p, int window, int sinks) {
   const int seen = min(max(p - t0 + 1, 0), 16), before = min(max(max(p - window + 1, 0) - t0, 0), 16),
             first = min(max(sinks - t0, 0), 16);
   return ((1u << seen) - 1u) & (~((1u << before) - 1u) | ((1u << first) - 1u));
+}
+
+// The largest |weight x value norm| of a row in a tile, at reference `ref`, from
+// the scores in tensor memory (infinite and NaN ones left out). Rare: a rolled
+// loop, so that the softmax's own code stays short.
+TQ_DEV float tw_largest(uint32_t scores, const TwSlot& s, float row_inv, float ref, int p, int window, int sinks) {
+  float most = 0.f;
+#pragma unroll 1
+  for (int c0 = 0; c0 < TW_TP; c0 += 8) {
+    uint32_t u[8];
+    tmem_ld8(scores + (uint32_t)c0, u);
+    tmem_wait_ld();
+    tmem_regs_after_wait(u);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float w = aw_exp2(__uint_as_float(u[c]) * s.nk[c0 + c] * row_inv - ref) * fabsf(s.nv[c0 + c]);
+      if (aw_visible(s.blk_t[c0 >> 4] + ((c0 + c) & 15), p, window, sinks)) most = fmaxf(most, w);
+    }
+  }
+  return most;
 }
 
 template <int N>
@@ -575,22 +596,29 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
           break;
         }
         TwSlot& s = reinterpret_cast<TwSlot*>(sm + C::N0)[i % TW_SLOTS];
-        float most = 0.f;
+        float most = 0.f, least = INFINITY;
         int t_min = INT_MAX, t_max = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int m = 4 * (tile0 + i) + 2 * h + q;
           const int at = m < bl.n ? aw_block(bl, m) * ATT_BLOCK : INT_MAX - 64;
           // a norm that no row sees takes no part in the power of two, whatever it is
-          if (!aw_seen(at + (lane & 15), p_lo, p_hi, a.window, a.sinks)) nv[h] = 0.f;
+          const bool seen = aw_seen(at + (lane & 15), p_lo, p_hi, a.window, a.sinks);
+          if (!seen) nv[h] = 0.f;
           const float v = fabsf(nv[h]);
-          if (v < INFINITY) most = fmaxf(most, v);
+          if (v < INFINITY) {
+            most = fmaxf(most, v);
+            if (seen) least = fminf(least, v);
+          }
           t_min = min(t_min, at);
           t_max = max(t_max, at + ATT_BLOCK - 1);
           if ((lane & 15) == 0) s.blk_t[2 * h + q] = at;
         }
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL, most, m));
+        for (int m = 16; m > 0; m >>= 1) {
+          most = fmaxf(most, __shfl_xor_sync(FULL, most, m));
+          least = fminf(least, __shfl_xor_sync(FULL, least, m));
+        }
         t_min = min(t_min, __shfl_xor_sync(FULL, t_min, 16));
         t_max = max(t_max, __shfl_xor_sync(FULL, t_max, 16));
         if (most > v_most) {
@@ -610,6 +638,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
           s.t_max = t_max;
           s.v_up = v_up;
           s.v_inv = v_inv;
+          s.nv_min = least * v_up;
         }
         if (i + 1 < cnt) fetch(i + 1);
         mbar_arrive(n_full + 8 * (i % TW_SLOTS));
@@ -698,6 +727,9 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
     const int pw_lo = any_row ? aw_position(sq, rw0 / a.g) : -1, pw_hi = any_row ? aw_position(sq, rw1 / a.g) : -1;
     const int p_row = row_ok ? aw_position(sq, q_i) : pw_hi;
     float m_ref = -INFINITY, l_sum = 0.f, v_inv = 1.f;
+    // a lower bound of the largest |weight x norm| of the row so far (infinite
+    // before the row's first position: no reason to move)
+    float w_low = INFINITY;
     bool ok = true;
     const int n = halves ? (cnt + 1 - mt) / 2 : cnt;
     for (int j = 0; j < n; ++j) {
@@ -754,39 +786,49 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
         mx0 = tw_max3(mx0, x[60], x[61]);
         mx1 = tw_max3(mx1, x[62], x[63]);
         const float mx = fmaxf(tw_max3(mx0, mx1, mx2), mx3) * row_inv;
-        // the reference follows the maximum when it is exceeded by 2^8
-        const bool move = mx > m_ref + 8.0f || (m_ref == -INFINITY && mx != -INFINITY);
         const float v_fix = slot.v_up * v_inv;  // over the power of two of the tile before
         v_inv = slot.v_inv;
-        float fix = v_fix;
-        if (move) {
-          const float f = aw_exp2(m_ref - mx);  // 0 from -inf
-          l_sum *= f;
-          fix *= f;
-          m_ref = mx;
-        }
-        if (j > 0 && __any_sync(FULL, move || v_fix != 1.0f)) {
-          // the previous product must be in the accumulator before it is
-          // rescaled. (Even and odd tiles have barriers of their own: a wait
-          // may be the first in many tiles, and this one's earlier phases
-          // ended before the scores of tile j - 1 were complete.)
-          const bool done = __all_sync(
-              FULL, tw_wait(o_done + 16 * mt + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, TW_TRIES));
-          if (!done) {
-            if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
-            ok = false;
-            break;
+        w_low *= v_fix;
+        // the reference follows a score that exceeds it by 2^8, and products that are small
+        const bool move = mx > m_ref + 8.0f || w_low < AW_SMALL;
+        if (__any_sync(FULL, move || v_fix != 1.0f)) {
+          float fix = v_fix;
+          const float top = fmaxf(m_ref, mx);
+          float most = slot.nv_min;  // at least, where the largest score is new
+          if (__any_sync(FULL, move && !(mx > m_ref && most >= AW_SMALL)))
+            most = tw_largest(sp, slot, row_inv, top, p_row, a.window, a.sinks);
+          if (move) {
+            const float old = aw_exp2(m_ref - top);  // 0 from -inf
+            most = fmaxf(most, w_low * old);  // (inf * 0 = NaN is left out)
+            const float to = aw_reference(top, l_sum * old, most), f = aw_exp2(m_ref - to);
+            l_sum *= f;
+            fix *= f;
+            m_ref = to;
+            w_low = most;
           }
-          tc_fence_after();
+          if (j > 0) {
+            // the previous product must be in the accumulator before it is
+            // rescaled. (Even and odd tiles have barriers of their own: a wait
+            // may be the first in many tiles, and this one's earlier phases
+            // ended before the scores of tile j - 1 were complete.)
+            const bool done = __all_sync(
+                FULL, tw_wait(o_done + 16 * mt + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, TW_TRIES));
+            if (!done) {
+              if (lane == 0) record_error(a.err, TQ_DEVERR_TIMEOUT);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 16) {
-            uint32_t u[16];
-            tmem_ld16(o0 + (uint32_t)c0, u);
-            tmem_wait_ld();
-            tmem_regs_after_wait(u);
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              uint32_t u[16];
+              tmem_ld16(o0 + (uint32_t)c0, u);
+              tmem_wait_ld();
+              tmem_regs_after_wait(u);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * fix);
-            tmem_st16(o0 + (uint32_t)c0, u);
+              for (int c = 0; c < 16; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * fix);
+              tmem_st16(o0 + (uint32_t)c0, u);
+            }
           }
         }
         const float ref = m_ref == -INFINITY ? 0.f : m_ref;

@@ -386,6 +386,79 @@ def test_norms_and_queries_of_any_size(K, k_norm, v_norm, q_size):
         _check(o, ref, tol)
 
 
+def _check_to_infinity(o, ref, tol):
+    """Results of any size: within the tolerance where fp16 holds the value,
+    infinite with the value's sign above. An element of a row with tolerance tol
+    is off by up to tol, so it is finite for certain where |value| + tol lies
+    below 65520 (where fp16 rounds to infinity), infinite where |value| - tol
+    lies above, and either one between (a row of 1e25 has elements that cancel
+    to 0 exactly, and a tolerance of 1e22)."""
+    o, size = o.cpu().double(), ref.abs()
+    fits, over = size + tol[..., None] < 65520, size - tol[..., None] > 65520
+    assert torch.isfinite(o[fits]).all()
+    assert torch.equal(o[over], ref[over].sign() * float("inf"))
+    err = torch.where(fits, o - ref, torch.zeros_like(ref)).norm(dim=-1)
+    assert (err <= tol).all(), (err / tol.clamp(min=1e-30)).max().item()
+
+
+@pytest.mark.parametrize("ratio", [1e4, 1e6, 1e10, 1e25])
+@pytest.mark.parametrize("n,hq,S", [(3, 2, 200), (3, 4, 3000), (64, 2, 200), (32, 2, 2000), (136, 4, 700)])
+@pytest.mark.parametrize("d,kb,vb", [(128, 2, 4), (64, 2, 2), (256, 2, 3)])
+def test_a_large_norm_leaves_the_rows_before_it_as_exact(K, d, kb, vb, n, hq, S, ratio):
+    """A value norm larger than the others by `ratio` at a token in the middle:
+    the rows of earlier tokens, in the same warp or row tile, do not see it and
+    are as exact as without it. Few and many query rows, one split and several."""
+    kc, kp, kn = _cache(K, (1, S, 2), d, kb, 1)
+    vc, vp, vn = _cache(K, (1, S, 2), d, vb, 2)
+    at = S - n + n // 2
+    vn[0, at] = ratio * vn.mean()
+    q = torch.randn(n, hq, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(n)).half()
+    o = K.attend_window(q, kc, vc, kp, kn, vp, vn, torch.tensor([S], dtype=torch.int32, device="cuda"),
+                        q_offsets=torch.tensor([0, n], dtype=torch.int32, device="cuda"), max_q=n)
+    kk, vv = R.decode_rows(kp[0], kn[0], kb, d), R.decode_rows(vp[0], vn[0], vb, d)
+    for i in sorted({0, 1, n // 2 - 1, n // 2, n - 1}):
+        ref, tol = R.attend(q[i][None], kk, vv, S - n + i + 1, None, 0, kb, vb)
+        _check_to_infinity(o[i][None], ref, tol)
+        assert ref.abs().max() > 0.01
+    assert K.tq_device_error() == (K.TQ_OK, 0)
+
+
+@pytest.mark.parametrize("weightless", [True, False])
+@pytest.mark.parametrize("n,S", [(1, 90), (4, 3000), (64, 90), (32, 2000)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_large_norms_at_small_weights(K, d, n, S, weightless):
+    """Visible positions whose weight and norm differ by large factors: one of
+    weight e^-45 whose norm is 2^40 times the others', and one that takes
+    nearly all the weight (others e^-28) while the others' norms are 2^43 times
+    its own (infinite rows for the tokens before it)."""
+    hq, kb, vb, at = 2, 2, 4, 37
+    g = torch.Generator(device="cuda").manual_seed(S + d)
+    u = torch.randn(d, generator=g, device="cuda")
+    u /= u.norm()
+    x = torch.randn(1, S, 1, d, generator=g, device="cuda")
+    x -= (x @ u)[..., None] * u  # other keys score near 0
+    gap = -45.0 if weightless else 28.0
+    x[0, at, 0] = gap * d ** 0.5 / 16 * u
+    kc = K.TurboQuant(d, kb)
+    kp, kn = kc.encode(x.half())
+    vc, vp, vn = _cache(K, (1, S, 1), d, vb, 2)
+    if weightless:
+        vn[0, at] *= 2.0 ** 40
+    else:
+        vn *= 2.0 ** 33
+        vn[0, at] = 2.0 ** -10 * d ** 0.5
+    q = (16 * u + 0.05 * torch.randn(n, hq, d, generator=g, device="cuda")).half()
+    o = K.attend_window(q, kc, vc, kp, kn, vp, vn, torch.tensor([S], dtype=torch.int32, device="cuda"),
+                        q_offsets=torch.tensor([0, n], dtype=torch.int32, device="cuda"), max_q=n)
+    kk, vv = R.decode_rows(kp[0], kn[0], kb, d), R.decode_rows(vp[0], vn[0], vb, d)
+    ref, tol = R.attend(q, kk, vv, S, None, 0, kb, vb)
+    sees = torch.arange(S - n, S) >= at
+    assert 0.001 < ref[sees].abs().max() < 60000
+    _check(o[sees.cuda()], ref[sees], tol[sees])
+    _check_to_infinity(o, ref, tol)
+    assert K.tq_device_error() == (K.TQ_OK, 0)
+
+
 def test_offsets_and_lengths_out_of_range_are_flagged(K):
     d, S, hq, hkv = 64, 32, 2, 1
     kc, kp, kn = _cache(K, (3, S, hkv), d, 4, 1)
