@@ -105,6 +105,13 @@ std::pair<uintptr_t, uintptr_t> span(const Tensor& t) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(t.data_ptr());
   return {a, a + (uintptr_t)(n * t.element_size())};
 }
+// Same strides, wherever there is a second element to step to.
+bool same_strides(const Tensor& a, const Tensor& b) {
+  if (a.sizes() != b.sizes()) return false;
+  for (int64_t i = 0; i < a.dim(); ++i)
+    if (a.size(i) > 1 && a.stride(i) != b.stride(i)) return false;
+  return true;
+}
 // Refuse an output that shares memory with another argument; with `itself`
 // only unless it is that very tensor.
 void apart(const char* name, const Tensor& out, std::initializer_list<const Tensor*> others, const Tensor* itself) {
@@ -114,7 +121,7 @@ void apart(const char* name, const Tensor& out, std::initializer_list<const Tens
     return lo < b && a < hi;
   };
   bool bad = itself && clash(*itself) &&
-             !(itself->data_ptr() == out.data_ptr() && itself->strides() == out.strides() &&
+             !(itself->data_ptr() == out.data_ptr() && same_strides(*itself, out) &&
                itself->scalar_type() == out.scalar_type());
   for (const Tensor* t : others) bad = bad || (t->defined() && clash(*t));
   if (bad) refuse(std::string(name) + ": shares memory with another argument");
@@ -167,9 +174,10 @@ void launching(int dev, const char* what, F&& f) {
   raise_status(st, what);
 }
 
-// Strides of a [T, H, d] view whose rows are dense and 16-byte aligned.
+// Strides of a [T, H, d] view whose rows are dense and 16-byte aligned (0 for a
+// dimension of one element, whose stride is never used and may be anything).
 std::pair<int64_t, int64_t> head_rows(const Tensor& t, const char* name) {
-  const int64_t s0 = t.stride(0), s1 = t.stride(1);
+  const int64_t s0 = t.size(0) > 1 ? t.stride(0) : 0, s1 = t.size(1) > 1 ? t.stride(1) : 0;
   if (t.stride(2) != 1 || ((s0 | s1) & 7) || (reinterpret_cast<uintptr_t>(t.data_ptr()) & 15))
     refuse(std::string(name) + ": dense rows, 16-byte aligned, strides multiples of 8 elements");
   return {s0, s1};

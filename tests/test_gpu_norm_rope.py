@@ -94,6 +94,24 @@ def test_in_place_strides_and_streams(K):
     assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
 
 
+def test_single_elements_of_any_stride(K):
+    """One token, and one head, of a buffer whose stride there is not a
+    multiple of 8 (it is never used), also in place."""
+    f, _ = K.rope_frequencies(128)
+    w = 1 + 0.1 * torch.randn(128, device="cuda")
+    wide = torch.randn(3, 6 * 128 + 5, device="cuda").half()
+    one = torch.randn(5, 8, 132, device="cuda").half()[:, :1, :128]
+    for q, k in ((wide.as_strided((1, 4, 128), (773, 128, 1)), wide.as_strided((1, 2, 128), (773, 128, 1), 512)),
+                 (one, torch.randn(5, 2, 128, device="cuda").half())):
+        pos = 7 + torch.arange(q.shape[0], dtype=torch.int32, device="cuda")
+        got = K.qk_norm_rope(q, k, pos, f, q_weight=w, k_weight=w)
+        _close(got[0], *R.rope(q, w, pos, f, False, 1.0, 1e-6))
+        _close(got[1], *R.rope(k, w, pos, f, False, 1.0, 1e-6))
+        if q.is_contiguous():
+            K.qk_norm_rope(q, k, pos, f, q_weight=w, k_weight=w, out=(q, k))
+            assert torch.equal(q, got[0]) and torch.equal(k, got[1])
+
+
 def test_empty_and_non_finite(K):
     q, k = _qkv(0, 4, 2, 128, torch.float16, 3)
     pos = torch.zeros(0, dtype=torch.int32, device="cuda")

@@ -58,6 +58,23 @@ def test_norm_rope_refusals(K):
     _raises(lambda: f_(q.transpose(1, 2).contiguous().transpose(1, 2), k, pos, f), "dense rows")
 
 
+def test_norm_rope_strides_of_single_elements(K):
+    """The stride of a dimension of one element is never used: any will do,
+    and a view that differs in it alone is the same tensor."""
+    pos, f = torch.zeros(1, dtype=torch.int32), K.rope_frequencies(128, device="cpu")[0]
+    wide = torch.zeros(3, 6 * 128 + 5, dtype=torch.float16)
+    q, k = wide.as_strided((1, 4, 128), (773, 128, 1)), wide.as_strided((1, 2, 128), (773, 128, 1), 512)
+    assert q.stride(0) % 8 and q.is_contiguous()
+    _raises(lambda: K.qk_norm_rope(q, k, pos, f), "CUDA")
+    one = torch.zeros(5, 8, 132, dtype=torch.float16)[:, :1, :128]  # one head, token strides of 8 x 132
+    assert one.stride(0) % 8 == 0 and one.stride(1) % 8
+    _raises(lambda: K.qk_norm_rope(one, one.clone(), torch.zeros(5, dtype=torch.int32), f), "CUDA")
+    # in place, through a view whose strides differ only where there is one element
+    _raises(lambda: K.qk_norm_rope(q, k, pos, f, out=(q.as_strided((1, 4, 128), (512, 128, 1)), k)), "CUDA")
+    _raises(lambda: K.qk_norm_rope(wide.as_strided((2, 4, 128), (773, 128, 1)), k.expand(2, 2, 128),
+                                   torch.zeros(2, dtype=torch.int32), f), "strides")
+
+
 def test_frequencies(K):
     f, s = K.rope_frequencies(64, 10000.0, device="cpu")
     assert f.dtype == torch.float64 and f.shape == (32,) and s == 1.0
