@@ -404,9 +404,14 @@ class TQPagedAttention:
         [T, Hkv, d] fp16 to slot_mapping [T] of the pools, then
         `attend_window_paged`. The tables and context_lens include the new
         tokens. Returns [T, num_query_heads, d] fp16."""
+        import torch
+
         _require(query.dim() == 3 and query.shape[1] == self.num_query_heads,
                  "query must be [T, num_query_heads, head_dim]")
         _require(value.dim() == 3 and value.shape == key.shape, "value: the key's shape")
+        _require(not (value.requires_grad and torch.is_grad_enabled()),
+                 "value: requires a gradient, which this call does not compute (detach it, or call under "
+                 "torch.no_grad())")
         q, k = qk_norm_rope(query, key, positions, inv_freq, interleaved=interleaved, rope_scale=rope_scale,
                             q_weight=q_weight, k_weight=k_weight, eps=eps, stream=stream)
         with _launching(q.device, stream):
@@ -508,7 +513,8 @@ def qk_norm_rope(q, k, positions, inv_freq=None, *, interleaved: bool = False, r
     in q's dtype or float32, None for no norm of that tensor. Returns (q, k)
     fp16 [T, H, d]: keys as `encode_slots` takes them, queries as the attention
     calls do. `out` = (q_out, k_out), which may be q and k where they are
-    contiguous fp16, and share no memory with the inputs otherwise.
+    contiguous fp16, and share no memory with the inputs otherwise. Forward
+    only: tensors that require a gradient are refused while one is recorded.
     """
     args = (q, k, positions, inv_freq, interleaved, rope_scale, q_weight, k_weight, eps, out)
     if stream is not None:
@@ -528,7 +534,7 @@ def attend_window(q, k_codec: TurboQuant, v_codec: TurboQuant, k_packed, k_norms
     tokens are q[q_offsets[b]:q_offsets[b + 1]], at most max_q of them (None:
     one token per sequence). Returns o [T, Hq, d] fp16 (rows of tokens in no
     sequence are not written). `out` may be q itself and shares no memory with
-    anything else.
+    anything else. Forward only, as `qk_norm_rope`.
     """
     args = (q, k_codec.ctx.address, v_codec.ctx.address, k_packed, k_norms, v_packed, v_norms, False, None,
             context_lens, window, sinks, q_offsets, max_q, out, workspace)

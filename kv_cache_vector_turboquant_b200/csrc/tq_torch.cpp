@@ -10,6 +10,7 @@
 // status. Outputs are allocated on the tensors' device, whose current stream
 // the call uses.
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -95,6 +96,16 @@ int one_device(std::initializer_list<std::pair<const char*, const Tensor*>> all)
              std::to_string(t->get_device()));
   }
   return dev;
+}
+
+// The calls have no backward pass: a tensor whose gradient is being recorded
+// would lose it without a word.
+void forward_only(std::initializer_list<std::pair<const char*, const Tensor*>> all) {
+  if (!c10::GradMode::is_enabled()) return;
+  for (const auto& [name, t] : all)
+    if (t->defined() && t->requires_grad())
+      refuse(std::string(name) + ": requires a gradient, which this call does not compute (detach it, or call under "
+             "torch.no_grad())");
 }
 
 // First address of a tensor and the first behind it.
@@ -226,6 +237,8 @@ py::tuple qk_norm_rope(py::handle q_, py::handle k_, py::handle positions_, py::
     apart("out q", qo, {&k, &ko, &positions, &inv_freq, &w[0], &w[1]}, &q);
     apart("out k", ko, {&q, &qo, &positions, &inv_freq, &w[0], &w[1]}, &k);
   }
+  forward_only({{"q", &q}, {"k", &k}, {"inv_freq", &inv_freq}, {"q_weight", &w[0]}, {"k_weight", &w[1]},
+                {"out q", &qo}, {"out k", &ko}});
   const int dev = one_device({{"q", &q}, {"k", &k}, {"positions", &positions}, {"inv_freq", &inv_freq},
                               {"q_weight", &w[0]}, {"k_weight", &w[1]}, {"out q", &qo}, {"out k", &ko}});
   check_sizes({hq, hkv});
@@ -292,6 +305,7 @@ Tensor attend_window(py::handle q_, uintptr_t k_codec, uintptr_t v_codec, py::ha
   if (workspace.defined()) check(workspace, "workspace", {ScalarType::Byte});
   if (out.defined()) apart("out", out, {&kc, &kn, &vc, &vn, &table, &lens, &offsets, &workspace}, &q);
   if (workspace.defined()) apart("workspace", workspace, {&q, &kc, &kn, &vc, &vn, &table, &lens, &offsets}, nullptr);
+  forward_only({{"q", &q}, {"k_norms", &kn}, {"v_norms", &vn}, {"out", &out}});
   const int dev = one_device({{"q", &q}, {"q_offsets", &offsets}, {"out", &out}, {"workspace", &workspace},
                               {k_name, &kc}, {v_name, &vc}, {"k_norms", &kn}, {"v_norms", &vn},
                               {"block_tables", &table}, {"context_lens", &lens}});

@@ -182,6 +182,38 @@ def test_window_refusals(K):
     _raises(lambda: layer.step(q, key, key, ctx, ctx, *pool, bt, ctx), "CUDA")
 
 
+def test_gradients_are_refused_not_dropped(K):
+    """No call here has a backward pass: what requires a gradient is refused
+    while gradients are recorded, and taken otherwise."""
+    q, k = torch.zeros(2, 4, 128, dtype=torch.float16), torch.zeros(2, 2, 128, dtype=torch.float16)
+    pos, w = torch.zeros(2, dtype=torch.int32), torch.nn.Parameter(torch.ones(128))
+    f = K.rope_frequencies(128, device="cpu")[0]
+    grad = lambda t: t.clone().requires_grad_()  # noqa: E731
+    f_ = K.qk_norm_rope
+    for name, call in (("q", lambda: f_(grad(q), k, pos, f)), ("k", lambda: f_(q, grad(k), pos, f)),
+                       ("q_weight", lambda: f_(q, k, pos, f, q_weight=w)),
+                       ("k_weight", lambda: f_(q, k, pos, f, k_weight=w)),
+                       ("inv_freq", lambda: f_(q, k, pos, grad(f))),
+                       ("out k", lambda: f_(q, k, pos, f, out=(q, grad(k))))):
+        _raises(call, f"^{name}: requires a gradient")
+        with torch.no_grad():
+            _raises(call, "CUDA")
+    _raises(lambda: f_(q, k, pos, f, q_weight=w.detach()), "CUDA")
+    kc, vc = K.TurboQuant(128, 4), K.TurboQuant(128, 2)
+    kp, vp = torch.zeros(2, 16, 2, 64, dtype=torch.uint8), torch.zeros(2, 16, 2, 32, dtype=torch.uint8)
+    kn, vn = torch.zeros(2, 16, 2), torch.zeros(2, 16, 2)
+    a = K.attend_window
+    for name, call in (("q", lambda: a(grad(q), kc, vc, kp, kn, vp, vn, pos)),
+                       ("k_norms", lambda: a(q, kc, vc, kp, grad(kn), vp, vn, pos)),
+                       ("v_norms", lambda: a(q, kc, vc, kp, kn, vp, grad(vn), pos)),
+                       ("q", lambda: K.attend_window_paged(grad(q), kc, vc, kp, kn, vp, vn, pos[:, None], pos)),
+                       ("value", lambda: K.TQPagedAttention(kc, 4, v_tq=vc).step(
+                           q, k, grad(k), pos, pos, kp, kn, vp, vn, pos[:, None], pos))):
+        _raises(call, f"^{name}: requires a gradient")
+        with torch.no_grad():
+            _raises(call, "CUDA")
+
+
 def test_page_refusals(K):
     t, n, r = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), torch.zeros(9, dtype=torch.int32)
     f = K.pages_trim
