@@ -431,7 +431,8 @@ tq_status tq_attend_window_paged(const tq_ctx* k, const tq_ctx* v, const void* q
  *   refs         [num_blocks] int32: how many rows list each page (<= 0: the
  *                page is free). The caller keeps it in line with the tables.
  * Every call reads one set of arrays and writes another; each output may be
- * its own input (in place), and must not overlap anything else. A table entry
+ * its own input (in place), and must not overlap anything else; workspaces and
+ * pools overlap no other argument. A table entry
  * at or above num_blocks that is met is dropped (-1) and flagged with
  * TQ_DEVERR_BLOCK_RANGE; a length above max_blocks * 16 counts as that and is
  * flagged with TQ_DEVERR_POS_RANGE. All calls are asynchronous on `stream`,

@@ -385,6 +385,21 @@ void on_pools(int dev, int pool_dev) {
     refuse("tensors on cuda:" + std::to_string(pool_dev) + " like the pools, got cuda:" + std::to_string(dev));
 }
 
+// Refuse tables and workspaces that share memory with a pool, whose pages the
+// call moves.
+void off_pools(const tq_page_pool* pools, int n_pools, int64_t num_blocks,
+               std::initializer_list<std::pair<const char*, const Tensor*>> all) {
+  for (const auto& [name, t] : all) {
+    if (!t->defined()) continue;
+    const auto [lo, hi] = span(*t);
+    for (int i = 0; i < n_pools; ++i) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(pools[i].base);
+      if (lo < a + (uintptr_t)(pools[i].block_bytes * num_blocks) && a < hi)
+        refuse(std::string(name) + ": shares memory with pool " + std::to_string(i));
+    }
+  }
+}
+
 // `pools`: address of `n_pools` tq_page_pool.
 py::tuple pages_fork(uintptr_t pools, int n_pools, int64_t num_blocks, int pool_dev, py::handle table_,
                      py::handle lens_, py::handle refs_, py::handle parents_, py::handle children_, py::handle out_,
@@ -407,6 +422,12 @@ py::tuple pages_fork(uintptr_t pools, int n_pools, int64_t num_blocks, int pool_
     apart("out", n, {&table, &refs, &t, &r, &parents, &children}, &lens);
     apart("out", r, {&table, &lens, &t, &n, &parents, &children}, &refs);
   }
+  if (workspace.defined())
+    apart("workspace", workspace, {&table, &lens, &refs, &parents, &children, &t, &n, &r}, nullptr);
+  const tq_page_pool* const of = reinterpret_cast<const tq_page_pool*>(pools);
+  off_pools(of, n_pools, num_blocks, {{"block_tables", &table}, {"context_lens", &lens}, {"refs", &refs},
+                                      {"parents", &parents}, {"children", &children}, {"workspace", &workspace},
+                                      {"out", &t}, {"out", &n}, {"out", &r}});
   const int dev = one_device({{"block_tables", &table}, {"context_lens", &lens}, {"refs", &refs},
                               {"parents", &parents}, {"children", &children}, {"workspace", &workspace}, {"out", &t},
                               {"out", &n}, {"out", &r}});
@@ -414,7 +435,7 @@ py::tuple pages_fork(uintptr_t pools, int n_pools, int64_t num_blocks, int pool_
   launching(dev, "tq_pages_fork", [&] {
     if (!t.defined()) t = fresh(table), n = fresh(lens), r = fresh(refs);
     if (!workspace.defined()) workspace = bytes_on(tq_pages_fork_workspace_bytes((int)forks), refs);
-    return tq_pages_fork(reinterpret_cast<const tq_page_pool*>(pools), n_pools, num_blocks, address_as<int32_t>(table),
+    return tq_pages_fork(of, n_pools, num_blocks, address_as<int32_t>(table),
                          address_as<int32_t>(t), address_as<int32_t>(lens), address_as<int32_t>(n),
                          address_as<int32_t>(refs), address_as<int32_t>(r), (int)rows, (int)table.size(1),
                          address_as<int32_t>(parents), address_as<int32_t>(children), (int)forks, address(workspace),
@@ -444,6 +465,10 @@ py::tuple pages_compact(uintptr_t pools, int n_pools, int64_t num_blocks, int po
     apart("out", remap, {&table, &refs, &t, &r, &used}, nullptr);
     apart("out", used, {&table, &refs, &t, &r, &remap}, nullptr);
   }
+  if (workspace.defined()) apart("workspace", workspace, {&table, &refs, &t, &r, &remap, &used}, nullptr);
+  const tq_page_pool* const of = reinterpret_cast<const tq_page_pool*>(pools);
+  off_pools(of, n_pools, num_blocks, {{"block_tables", &table}, {"refs", &refs}, {"workspace", &workspace},
+                                      {"out", &t}, {"out", &r}, {"out remap", &remap}, {"out used", &used}});
   const int dev = one_device({{"block_tables", &table}, {"refs", &refs}, {"workspace", &workspace}, {"out", &t},
                               {"out", &r}, {"out", &remap}, {"out", &used}});
   on_pools(dev, pool_dev);
@@ -453,7 +478,7 @@ py::tuple pages_compact(uintptr_t pools, int n_pools, int64_t num_blocks, int po
       used = at::empty({1}, refs.options());
     }
     if (!workspace.defined()) workspace = bytes_on(tq_pages_compact_workspace_bytes(num_blocks), refs);
-    return tq_pages_compact(reinterpret_cast<const tq_page_pool*>(pools), n_pools, num_blocks,
+    return tq_pages_compact(of, n_pools, num_blocks,
                             address_as<int32_t>(table), address_as<int32_t>(t), address_as<int32_t>(refs),
                             address_as<int32_t>(r), (int)table.size(0), (int)table.size(1),
                             address_as<int32_t>(remap), address_as<int32_t>(used), address(workspace),

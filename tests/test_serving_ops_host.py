@@ -245,6 +245,50 @@ def test_page_refusals(K):
     _raises(lambda: P([torch.zeros(9, 16, dtype=torch.uint8) for _ in range(513)]), "512")
 
 
+def test_page_calls_refuse_shared_memory(K):
+    """Workspaces, tables and outputs of fork and compact that share memory
+    with one another or with a pool (host tensors; every refusal comes before
+    the one of their device)."""
+    ops, i32 = K._calls(), torch.int32
+    pool = torch.zeros(9, 16, 2, 16, dtype=torch.uint8)
+    a = (K.PagePool * 1)()
+    a[0].base, a[0].block_bytes = pool.data_ptr(), 512
+    mine = (ctypes.addressof(a), 1, 9, 0)
+
+    def fork(t=None, n=None, r=None, p=None, c=None, out=None, ws=None):
+        new = lambda x, *s: torch.zeros(*s, dtype=i32) if x is None else x  # noqa: E731
+        return lambda: ops.pages_fork(*mine, new(t, 3, 4), new(n, 3), new(r, 9), new(p, 2), new(c, 2), out, ws)
+
+    def compact(t=None, r=None, out=None, ws=None):
+        new = lambda x, *s: torch.zeros(*s, dtype=i32) if x is None else x  # noqa: E731
+        return lambda: ops.pages_compact(*mine, new(t, 3, 4), new(r, 9), out, ws)
+
+    slab = torch.zeros(4096, dtype=torch.uint8)
+    word = lambda at, *s: slab[at:at + 4 * math.prod(s)].view(i32).view(*s)  # noqa: E731
+    for call in (fork(), compact(), fork(ws=slab), compact(ws=slab), fork(t=word(0, 3, 4), ws=slab[48:])):
+        _raises(call, "CUDA")  # nothing shared
+    out = (torch.zeros(3, 4, dtype=i32), torch.zeros(3, dtype=i32), torch.zeros(9, dtype=i32))
+    for call in (fork(t=word(0, 3, 4), ws=slab), fork(n=word(64, 3), ws=slab), fork(r=word(64, 9), ws=slab),
+                 fork(p=word(64, 2), ws=slab), fork(c=word(0, 2), ws=slab[4:]),
+                 fork(out=(word(0, 3, 4), *out[1:]), ws=slab[44:]), fork(out=(out[0], word(0, 3), out[2]), ws=slab),
+                 fork(out=(*out[:2], word(4060, 9)), ws=slab[:4064]),
+                 compact(t=word(0, 3, 4), ws=slab), compact(r=word(64, 9), ws=slab),
+                 compact(out=(word(0, 3, 4), out[2], torch.zeros(9, dtype=i32), torch.zeros(1, dtype=i32)), ws=slab),
+                 compact(out=(out[0], out[2], word(64, 9), torch.zeros(1, dtype=i32)), ws=slab),
+                 compact(out=(out[0], out[2], torch.zeros(9, dtype=i32), word(64, 1)), ws=slab)):
+        _raises(call, "workspace: shares memory with another")
+    inside = lambda *s: pool.view(-1)[-4 * math.prod(s):].view(i32).view(*s)  # noqa: E731
+    for call, name in ((fork(t=inside(3, 4)), "block_tables"), (fork(n=inside(3)), "context_lens"),
+                       (fork(r=inside(9)), "refs"), (fork(p=inside(2)), "parents"), (fork(c=inside(2)), "children"),
+                       (fork(ws=pool.view(-1)[16:]), "workspace"), (fork(out=(inside(3, 4), *out[1:])), "out"),
+                       (fork(out=(out[0], inside(3), out[2])), "out"), (fork(out=(*out[:2], inside(9))), "out"),
+                       (compact(t=inside(3, 4)), "block_tables"), (compact(r=inside(9)), "refs"),
+                       (compact(ws=pool.view(-1)[16:]), "workspace"),
+                       (compact(out=(out[0], out[2], inside(9), torch.zeros(1, dtype=i32))), "out remap"),
+                       (compact(out=(out[0], out[2], torch.zeros(9, dtype=i32), inside(1))), "out used")):
+        _raises(call, f"^{name}: shares memory with pool 0")
+
+
 def test_abi_refusals(K):
     """The C entry points with host pointers that are never followed."""
     L = K._binding._lib
