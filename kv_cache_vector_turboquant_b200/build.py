@@ -1,5 +1,6 @@
 """Build libtq.so in-tree with nvcc for sm_100a, and _ops.so (argument checks and
-calls for PyTorch tensors, linked against libtq.so and torch) beside it.
+calls for PyTorch tensors, linked against libtq.so and torch) beside it. Without
+an installed torch only _ops.so is left out.
 
 Usage: ``python kv_cache_vector_turboquant_b200/build.py [--force] [-j N]`` (run as a
 script: importing the package would load the library being built).
@@ -46,12 +47,17 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _torch() -> str:
-    """Directory of the installed torch (found without importing it)."""
+def _torch() -> str | None:
+    """Directory of the installed torch (found without importing it), or None."""
     spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("torch not found")
-    return spec.submodule_search_locations[0]
+    return None if spec is None else spec.submodule_search_locations[0]
+
+
+def _abi(torch: str) -> str:
+    """What _ops.so is compiled and linked against: torch's place and version
+    and Python's ABI."""
+    with open(os.path.join(torch, "version.py")) as f:
+        return "\n".join([torch, f.read(), str(sysconfig.get_config_var("SOABI")), sysconfig.get_paths()["include"]])
 
 
 def _headers() -> list[str]:
@@ -69,18 +75,23 @@ def _stale(target: str, deps: list[str]) -> bool:
 
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
     """Compile every source for sm_100a, link libtq.so, libtq_test.so and
-    _ops.so; return the path of libtq.so."""
+    (where torch is installed) _ops.so; return the path of libtq.so."""
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     headers = _headers()
     objs, test_objs, ops_objs, todo = [], [], [], []
     torch = _torch()
-    for srcs, out in ((SOURCES, objs), (TEST_SOURCES, test_objs), (OPS_SOURCES, ops_objs)):
+    # the torch and Python that the objects of _ops.so were compiled for
+    stamp, abi, old_abi = os.path.join(BUILD, "ops_abi.txt"), _abi(torch) if torch else None, None
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            old_abi = f.read()
+    for srcs, out in ((SOURCES, objs), (TEST_SOURCES, test_objs), (OPS_SOURCES if torch else [], ops_objs)):
         for src in srcs:
             path = os.path.join(CSRC, src)
             obj = os.path.join(BUILD, src + ".o")
             out.append(obj)
-            if force or _stale(obj, [path] + headers):
+            if force or _stale(obj, [path] + headers) or (out is ops_objs and abi != old_abi):
                 todo.append((path, obj))
 
     def compile_one(item):
@@ -115,7 +126,9 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         if r.returncode != 0:
             raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, TEST_LIB)
-    if force or todo or _stale(OPS_LIB, ops_objs + [LIB]):
+    if not torch:
+        print("torch not found: _ops.so is not built", file=sys.stderr)
+    elif force or todo or _stale(OPS_LIB, ops_objs + [LIB]):
         tmp = OPS_LIB + ".tmp"
         cmd = [nvcc, "-shared", "-cudart", "none", "-o", tmp] + ops_objs + [
             "-L" + PKG, "-ltq", "-Xlinker", "-rpath", "-Xlinker", "$ORIGIN", "-L" + os.path.join(torch, "lib"),
@@ -124,6 +137,8 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         if r.returncode != 0:
             raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, OPS_LIB)
+        with open(stamp, "w") as f:
+            f.write(abi)
     return LIB
 
 
