@@ -403,7 +403,8 @@ class TQPagedAttention:
         key [T, Hkv, d] at `positions` [T], `encode_slots` of keys and values
         [T, Hkv, d] fp16 to slot_mapping [T] of the pools, then
         `attend_window_paged`. The tables and context_lens include the new
-        tokens. Returns [T, num_query_heads, d] fp16."""
+        tokens. Returns [T, num_query_heads, d] fp16. Arguments are refused
+        before anything is written to the pools."""
         import torch
 
         _require(query.dim() == 3 and query.shape[1] == self.num_query_heads,
@@ -414,6 +415,12 @@ class TQPagedAttention:
                  "torch.no_grad())")
         q, k = qk_norm_rope(query, key, positions, inv_freq, interleaved=interleaved, rope_scale=rope_scale,
                             q_weight=q_weight, k_weight=k_weight, eps=eps, stream=stream)
+        _require(value.device == q.device, f"value: on {q.device} like the query, got {value.device}")
+        _check(slot_mapping, "slot_mapping", torch.int32, numel=key.shape[0])
+        _require(slot_mapping.device == q.device, f"slot_mapping: on {q.device} like the query, got {slot_mapping.device}")
+        _calls().check_attend_window(q, self.k_codec.ctx.address, self.v_codec.ctx.address, k_packed, k_norms,
+                                     v_packed, v_norms, True, block_tables, context_lens, window, sinks, q_offsets,
+                                     max_q, None, None)
         with _launching(q.device, stream):
             value = value.half().contiguous()
             self.k_codec.encode_slots(k, k_packed, k_norms, slot_mapping)

@@ -260,7 +260,9 @@ py::tuple qk_norm_rope(py::handle q_, py::handle k_, py::handle positions_, py::
 // ------------------------------------------------------------------ windowed attention
 
 // Both forms: `table` undefined for contiguous caches. `k_codec`, `v_codec`:
-// addresses of the codecs' contexts.
+// addresses of the codecs' contexts. With RUN false the arguments are only
+// checked.
+template <bool RUN>
 Tensor attend_window(py::handle q_, uintptr_t k_codec, uintptr_t v_codec, py::handle kc_, py::handle kn_,
                      py::handle vc_, py::handle vn_, bool paged, py::handle table_, py::handle lens_,
                      py::handle window_, py::handle sinks_, py::handle offsets_, py::handle max_q_, py::handle out_,
@@ -310,6 +312,7 @@ Tensor attend_window(py::handle q_, uintptr_t k_codec, uintptr_t v_codec, py::ha
                               {k_name, &kc}, {v_name, &vc}, {"k_norms", &kn}, {"v_norms", &vn},
                               {"block_tables", &table}, {"context_lens", &lens}});
   check_sizes({B, max_q, hq, hkv, paged ? table.size(1) : 0});
+  if (!RUN) return q;
   launching(dev, paged ? "tq_attend_window_paged" : "tq_attend_window", [&] {
     if (!out.defined()) out = at::empty({T, hq, d}, q.options());
     if (!workspace.defined())
@@ -491,7 +494,8 @@ py::tuple pages_compact(uintptr_t pools, int n_pools, int64_t num_blocks, int po
 
 PYBIND11_MODULE(_ops, m) {
   m.def("qk_norm_rope", &qk_norm_rope);
-  m.def("attend_window", &attend_window);
+  m.def("attend_window", &attend_window<true>);
+  m.def("check_attend_window", &attend_window<false>);
   m.def("pages_trim", &pages_trim);
   m.def("pages_fork", &pages_fork);
   m.def("pages_compact", &pages_compact);

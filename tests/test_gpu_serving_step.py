@@ -18,6 +18,33 @@ def K(cuda_device):
     return K
 
 
+def test_a_refused_step_leaves_the_pools_as_they_were(K):
+    d, hq, hkv, T = 64, 4, 2, 3
+    kc, vc = K.TurboQuant(d, 4), K.TurboQuant(d, 2)
+    layer = K.TQPagedAttention(kc, hq, v_tq=vc)
+    pools = [torch.zeros(4, 16, hkv, kc.packed_bytes, dtype=torch.uint8, device="cuda"),
+             torch.zeros(4, 16, hkv, device="cuda"),
+             torch.zeros(4, 16, hkv, vc.packed_bytes, dtype=torch.uint8, device="cuda"),
+             torch.zeros(4, 16, hkv, device="cuda")]
+    q, k, v = (torch.randn(T, h, d, device="cuda").half() for h in (hq, hkv, hkv))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    good = {"positions": i32([0, 1, 2]), "slot_mapping": i32([0, 1, 2]), "k_packed": pools[0], "k_norms": pools[1],
+            "v_packed": pools[2], "v_norms": pools[3], "block_tables": i32([[0]]), "context_lens": i32([3]),
+            "q_offsets": i32([0, 3]), "max_q": 3}
+    for bad in ({"window": 0}, {"sinks": -1}, {"q_offsets": None}, {"max_q": None}, {"context_lens": i32([3, 3])},
+                {"context_lens": i32([3]).long()}, {"block_tables": i32([0])}, {"v_norms": pools[3][:3]},
+                {"v_packed": pools[0]}, {"k_norms": pools[1].double()}, {"slot_mapping": i32([0, 1])},
+                {"slot_mapping": i32([0, 1, 2]).long()}, {"slot_mapping": i32([0, 1, 2]).cpu()},
+                {"context_lens": i32([3]).cpu()}, {"positions": i32([0, 1])}):
+        with pytest.raises(ValueError):
+            layer.step(q, k, v, **(good | bad))
+        with pytest.raises(ValueError):
+            layer.step(q, k, v.cpu(), **good)
+        assert not any(p.any() for p in pools), bad
+    o = layer.step(q, k, v, **good)
+    assert torch.isfinite(o).all() and all(p[0, :3].any() for p in pools)
+
+
 def test_prompt_decode_fork_trim_compact(K):
     d, hq, hkv, kb, vb, window, sinks = 64, 6, 2, 4, 3, 40, 5
     rows, mb, nb = 4, 12, 30
