@@ -459,6 +459,26 @@ def test_large_norms_at_small_weights(K, d, n, S, weightless):
     assert K.tq_device_error() == (K.TQ_OK, 0)
 
 
+@pytest.mark.parametrize("k_norm,v_norm,q_size", [(1e6, 1e6, 1e-4), (1e-6, 1e-6, 100.0), (1e-30, 1e4, 1.0),
+                                                  (30.0, 1e-20, 1e-3), (1e-3, 3e6, 1.0), (1e4, 2e5, 1e-3)])
+@pytest.mark.parametrize("n,hq", [(1, 4), (5, 4), (64, 2)])
+@pytest.mark.parametrize("d,kb,vb", [(64, 4, 3), (128, 4, 2), (256, 3, 4)])
+def test_norms_of_any_size_up_to_infinity(K, d, kb, vb, n, hq, k_norm, v_norm, q_size):
+    """Norms and queries of any size that every query looks at, few and many
+    query rows: finite where fp16 holds the result, infinite above."""
+    S, L = 100, 97
+    kc, kp, kn = _cache(K, (1, S, 1), d, kb, 1)
+    vc, vp, vn = _cache(K, (1, S, 1), d, vb, 2)
+    kn, vn = kn / kn.mean() * k_norm, vn / vn.mean() * v_norm
+    q = (q_size * torch.randn(n, hq, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(d))).half()
+    o = K.attend_window(q, kc, vc, kp, kn, vp, vn, torch.tensor([L], dtype=torch.int32, device="cuda"),
+                        q_offsets=torch.tensor([0, n], dtype=torch.int32, device="cuda"), max_q=n)
+    kk, vv = R.decode_rows(kp[0, :L], kn[0, :L], kb, d), R.decode_rows(vp[0, :L], vn[0, :L], vb, d)
+    ref, tol = R.attend(q, kk, vv, L, None, 0, kb, vb)
+    _check_to_infinity(o, ref, tol)
+    assert K.tq_device_error() == (K.TQ_OK, 0)
+
+
 def test_offsets_and_lengths_out_of_range_are_flagged(K):
     d, S, hq, hkv = 64, 32, 2, 1
     kc, kp, kn = _cache(K, (3, S, hkv), d, 4, 1)
