@@ -13,6 +13,7 @@ import os
 import re
 import shutil
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 
@@ -90,3 +91,28 @@ def test_cuda_core_encode_has_no_stack_frame(tmp_path_factory, bits):
     frames = _frames("tq_encode.cu", tmp_path_factory.mktemp("enc"))
     hits = [v for k, v in frames.items() if re.search(rf"encode_kernelILi128ELi{bits}E", k)]
     assert hits and all(v == (0, 0, 0) for v in hits), hits
+
+
+def test_norm_and_rotation_have_no_stack_frame(tmp_path_factory):
+    frames = _frames("tq_norm_rope.cu", tmp_path_factory.mktemp("norm_rope"))
+    hits = [v for k, v in frames.items() if "norm_rope_kernel" in k]
+    assert len(hits) == 18 and all(v == (0, 0, 0) for v in hits), frames
+
+
+def test_windowed_attention_frames(tmp_path_factory):
+    """Their arrays stay in registers: of the few-row kernel, the instances at
+    128 registers (head_dim 128, up to 4 query rows) spill a few words, of the
+    tcgen05 kernel every instance (none of them an array: the smallest, a
+    thread's 32 scores of a half tile, has 128 bytes)."""
+    with ThreadPoolExecutor(2) as ex:
+        few, many = ex.map(lambda f: _frames(f, tmp_path_factory.mktemp("window")),
+                           ["tq_attend_window.cu", "tq_attend_window_tc.cu"])
+    hits = [(k, v) for k, v in few.items() if "window_partial_kernel" in k]
+    assert len(hits) == 45
+    for k, (frame, store, load) in hits:
+        most = 32 if re.search(r"window_partial_kernelILi128ELi\dELi\dELi1E", k) else 0
+        assert max(frame, store, load) <= most, (k, frame, store, load)
+    hits = [(k, v) for k, v in many.items() if "window_tc_kernel" in k]
+    assert len(hits) == 27
+    for k, (frame, store, load) in hits:
+        assert frame <= 32 and store <= 32 and load <= 96, (k, frame, store, load)
