@@ -39,7 +39,7 @@
 // two that follows the largest value norm that a row of the warp sees (up to
 // 2^14: nothing overflows). A row whose own products are much smaller takes a
 // lower reference for its weights (aw_reference), so each product is off by
-// 2^-22 of itself or 2^-26 of the row's largest, whatever other rows see, for
+// 2^-22 of itself or 2^-23 of the row's largest, whatever other rows see, for
 // norms within 2^90 of the largest. The reference moves only when a score
 // exceeds it by more than 2^8 or the row's products are small (exact: sum and
 // accumulator share it).

@@ -142,18 +142,20 @@ TQ_DEV float aw_pow2_for(float mag, float& inv) {
 // The reference that a row's weights w_t = 2^(s_t - ref) refer to is free: the
 // row's sum and accumulator share it. It is the row's largest score, unless the
 // largest weight x value norm (times the tile's power of two, below 64) would
-// then lie below AW_SMALL, where its fp16 remainder runs out of bits: norms that
-// this row does not see, or positions that it gives no weight, may be larger by
-// any factor. Then the reference is lowered until that product lies in
-// [2^5, 2^6), or the row's sum of weights near 2^AW_SUM.
-constexpr float AW_SMALL = 2.0f;
+// then lie below AW_SMALL, where its fp16 remainder (a multiple of 2^-24) runs
+// out of bits: norms that this row does not see, or positions that it gives no
+// weight, may be larger by any factor. Then the reference is lowered until that
+// product lies in [2^2, 2^3), or the row's sum of weights near 2^AW_SUM. (With 2
+// for AW_SMALL and [2^5, 2^6), 2 x 2048 tokens whose norms spread by e^1 took
+// 1018 us, with these 734, both before tw_largest took logarithms.)
+constexpr float AW_SMALL = 0.25f;
 constexpr int AW_SUM = 100;
 // Reference for a row whose scores have reached `top`, at which its sum is `sum`
 // and its largest weight x norm `most`, which becomes the one at the result.
 TQ_DEV float aw_reference(float top, float sum, float& most) {
   if (most >= AW_SMALL || !(most > 0.f)) return top;
   const int e = (int)(__float_as_uint(most) >> 23) - 127, e_sum = (int)(__float_as_uint(sum) >> 23) - 127;
-  const int low = max(min(5 - e, AW_SUM - max(e_sum, 0)), 0);
+  const int low = max(min(2 - e, AW_SUM - max(e_sum, 0)), 0);
   most *= __uint_as_float((uint32_t)(127 + low) << 23);
   return top - (float)low;
 }

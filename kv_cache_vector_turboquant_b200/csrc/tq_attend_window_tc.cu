@@ -24,7 +24,8 @@
 //  * 4 warps per row tile, one row per thread: scores from tensor memory,
 //    times the key norm, running maximum, weights times value norms as fp16
 //    value + remainder back to tensor memory, over the scores. The reference
-//    of the weights moves only when a score exceeds it by more than 2^8 or the
+//    of the weights moves only when a weight times the tile's norms could
+//    pass 2^14 (a score 2^8 above it where the tile holds the largest norm) or the
 //    row's products with the norms are small (aw_reference; exact: sum and
 //    accumulator share it), so the accumulator is rescaled rarely.
 // Scores are double-buffered: the next tile's S is computed while the
@@ -69,12 +70,13 @@ constexpr int TW_TMEM = 512;
 struct TwSlot {
   float nk[TW_TP];
   float nv[TW_TP];   // times the power of two of the tile
+  float lg[TW_TP];   // log2 |nv|
   int blk_t[4];      // first position of each 16-position block (INT_MAX - 64: none)
   int t_min, t_max;  // first and last position
   float v_up, v_inv; // this tile's power of two and its inverse
   uint32_t odd[2];   // positions whose value norm is infinite or NaN (0 in nv)
   float nv_min;      // smallest finite |nv| that a row sees
-  int pad;
+  float head;        // weights up to 2^head times the tile's norms stay below 2^14
 };
 
 template <int D, int KB, int VB>
@@ -224,24 +226,23 @@ TQ_DEV uint32_t tw_visible16(int t0, int p, int window, int sinks) {
   return ((1u << seen) - 1u) & (~((1u << before) - 1u) | ((1u << first) - 1u));
 }
 
-// The largest |weight x value norm| of a row in a tile, at reference `ref`, from
-// the scores in tensor memory (infinite and NaN ones left out). Rare: a rolled
-// loop, so that the softmax's own code stays short.
-TQ_DEV float tw_largest(uint32_t scores, const TwSlot& s, float row_inv, float ref, int p, int window, int sinks) {
-  float most = 0.f;
-#pragma unroll 1
-  for (int c0 = 0; c0 < TW_TP; c0 += 8) {
-    uint32_t u[8];
-    tmem_ld8(scores + (uint32_t)c0, u);
-    tmem_wait_ld();
-    tmem_regs_after_wait(u);
+// log2 of the largest |weight x value norm| of a row in a tile at reference 0
+// (masked scores are -inf; NaN ones are left out). In logarithms: with 64
+// exponentials from a rolled loop over tensor memory an evaluation took the
+// warp some 6000 cycles, and 2 x 2048 tokens whose norms spread by e^1 734 us
+// instead of 595 (by e^0.2 583 and 593: the longer code costs that much).
+TQ_DEV float tw_largest(const float (&x)[64], const float* lg, float row_inv) {
+  const f2 scale = make_float2(row_inv, row_inv);
+  float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const float w = aw_exp2(__uint_as_float(u[c]) * s.nk[c0 + c] * row_inv - ref) * fabsf(s.nv[c0 + c]);
-      if (aw_visible(s.blk_t[c0 >> 4] + ((c0 + c) & 15), p, window, sinks)) most = fmaxf(most, w);
-    }
+  for (int c = 0; c < 64; c += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(lg + c);
+    const f2 u = fma2(make_float2(x[c], x[c + 1]), scale, make_float2(l.x, l.y));
+    const f2 v = fma2(make_float2(x[c + 2], x[c + 3]), scale, make_float2(l.z, l.w));
+    m0 = tw_max3(m0, u.x, u.y);
+    m1 = tw_max3(m1, v.x, v.y);
   }
-  return most;
+  return fmaxf(m0, m1);
 }
 
 template <int N>
@@ -629,7 +630,9 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
         for (int h = 0; h < 2; ++h) {
           const bool fine = fabsf(nv[h]) < INFINITY;
           s.nk[32 * h + lane] = nk[h];
-          s.nv[32 * h + lane] = fine ? nv[h] * v_up : 0.f;
+          const float n = fine ? nv[h] * v_up : 0.f;
+          s.nv[32 * h + lane] = n;
+          s.lg[32 * h + lane] = __log2f(fabsf(n));
           const uint32_t odd = __ballot_sync(FULL, !fine);
           if (lane == 0) s.odd[h] = odd;
         }
@@ -639,6 +642,7 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
           s.v_up = v_up;
           s.v_inv = v_inv;
           s.nv_min = least * v_up;
+          s.head = (float)min(13 - ((int)(__float_as_uint(most * v_up) >> 23) - 127), 30);
         }
         if (i + 1 < cnt) fetch(i + 1);
         mbar_arrive(n_full + 8 * (i % TW_SLOTS));
@@ -789,14 +793,14 @@ __global__ void __launch_bounds__(TwCfg<D, KB, VB>::WARPS * 32, 1)
         const float v_fix = slot.v_up * v_inv;  // over the power of two of the tile before
         v_inv = slot.v_inv;
         w_low *= v_fix;
-        // the reference follows a score that exceeds it by 2^8, and products that are small
-        const bool move = mx > m_ref + 8.0f || w_low < AW_SMALL;
+        // the reference follows products that could pass 2^14, and ones that are small
+        const bool move = mx > m_ref + slot.head || w_low < AW_SMALL;
         if (__any_sync(FULL, move || v_fix != 1.0f)) {
           float fix = v_fix;
           const float top = fmaxf(m_ref, mx);
           float most = slot.nv_min;  // at least, where the largest score is new
           if (__any_sync(FULL, move && !(mx > m_ref && most >= AW_SMALL)))
-            most = tw_largest(sp, slot, row_inv, top, p_row, a.window, a.sinks);
+            most = aw_exp2(tw_largest(x, slot.lg, row_inv) - top);
           if (move) {
             const float old = aw_exp2(m_ref - top);  // 0 from -inf
             most = fmaxf(most, w_low * old);  // (inf * 0 = NaN is left out)

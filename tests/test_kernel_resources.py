@@ -115,4 +115,4 @@ def test_windowed_attention_frames(tmp_path_factory):
     hits = [(k, v) for k, v in many.items() if "window_tc_kernel" in k]
     assert len(hits) == 27
     for k, (frame, store, load) in hits:
-        assert frame <= 32 and store <= 32 and load <= 96, (k, frame, store, load)
+        assert frame <= 32 and store <= 32 and load <= 128, (k, frame, store, load)
