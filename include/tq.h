@@ -337,7 +337,8 @@ tq_status tq_attend_decode_static(const tq_ctx* k, const tq_ctx* v, const void* 
  *                               y_b cos(p f_i) + y_a sin(p f_i)),  i < rot_dim / 2
  * with (a, b) = (2 i, 2 i + 1) if `interleaved`, else (i, i + rot_dim / 2);
  * coordinates from rot_dim on are not rotated (nor scaled). Computed in f32
- * with the angle reduced in f64, rounded once to fp16.
+ * with the angle reduced in f64, rounded once to fp16 (a bf16 row whose sum of
+ * squares passes f32's range, so with coordinates near 1e18, is normed to 0).
  *   q, k        device, n_tok x hq (hkv) rows of head_dim elements of `dtype`,
  *               row (t, h) at element t * tok_stride + h * head_stride; 16-byte
  *               aligned, strides multiples of 8 (views of one projection's
@@ -393,13 +394,24 @@ size_t tq_attend_window_workspace_bytes(int64_t n_tok, int B, int max_q, int hq,
  *               TQ_DEVERR_POS_RANGE.
  *   window      >= 1, or <= 0 for no limit.   sinks: >= 0.
  *   k_cache ... as tq_attend_decode: [B, s_max, hkv, P] and norms
- *               [B, s_max, hkv]; positions that no query sees are not read.
+ *               [B, s_max, hkv]; blocks of 16 positions that no query sees
+ *               and rows behind a context are not read, and what stands at
+ *               other positions that a query does not see takes no part in
+ *               its row, whatever it is.
  *   out_f16     device, [n_tok, hq, d] fp16 out, 16-byte aligned; may be
  *               q_f16 itself, and overlaps nothing else.
  *   workspace   at least tq_attend_window_workspace_bytes(...) bytes, 16-byte
  *               aligned (NULL if that is 0); contents on entry do not matter.
  * Any hq that is a multiple of hkv; hkv at most 65536, s_max below 2^31 - 256,
  * B at most 65535.
+ * Precision: sums, maxima and scores are f32. Of the products' fp16 operands the
+ * codebook levels lie within 1.7e-6 (2 bits), 1.5e-5 (3) and 7.0e-5 (4) of a
+ * level; query coordinates, and weights times value norms, are two fp16 parts
+ * (22 bits of themselves; 23 bits of a row's largest product, for value norms
+ * within 2^90 of the largest in sight).
+ * One kernel and one number of splits serve all sequences of a call, chosen from
+ * the sizes passed (max_q, not a sequence's own tokens). A batch of prompt
+ * chunks and single tokens is faster in two calls, the long ones and the others.
  * Asynchronous on `stream`; calls that share a workspace must not overlap.
  */
 tq_status tq_attend_window(const tq_ctx* k, const tq_ctx* v, const void* q_f16, int64_t n_tok, int B,
@@ -475,7 +487,9 @@ tq_status tq_pages_fork(const tq_page_pool* pools, int n_pools, int64_t num_bloc
  * with this window and sinks sees from the row's last token on: pages that
  * hold no position below `sinks` and end at or before lens - window. Their
  * entries become -1 and their refs go down by one.
- *   window      >= 0, or < 0 for no window (rows are only released).
+ *   window      >= 0, or < 0 for no window (rows are only released). Here 0
+ *               is a window of no positions, where tq_attend_window's 0 is no
+ *               limit: pass that as -1.
  *   release     device, [n_rows] uint8, or NULL.
  */
 tq_status tq_pages_trim(const int32_t* block_tables, int32_t* tables_out, const int32_t* lens, int32_t* lens_out,

@@ -542,6 +542,12 @@ def attend_window(q, k_codec: TurboQuant, v_codec: TurboQuant, k_packed, k_norms
     one token per sequence). Returns o [T, Hq, d] fp16 (rows of tokens in no
     sequence are not written). `out` may be q itself and shares no memory with
     anything else. Forward only, as `qk_norm_rope`.
+
+    Sums and scores are float32; codebook levels enter the products as fp16
+    (within 7e-5 of a level at 4 bits, 1.5e-5 at 3, 1.7e-6 at 2), queries and
+    weights times norms as two fp16 parts (22 bits). One kernel and one number
+    of splits serve the whole call, chosen from max_q: prompt chunks and single
+    tokens of one batch are faster in two calls.
     """
     args = (q, k_codec.ctx.address, v_codec.ctx.address, k_packed, k_norms, v_packed, v_norms, False, None,
             context_lens, window, sinks, q_offsets, max_q, out, workspace)
@@ -567,7 +573,8 @@ def attend_window_paged(q, k_codec: TurboQuant, v_codec: TurboQuant, k_cache, k_
 def pages_trim(block_tables, context_lens, refs, window=None, sinks: int = 0, release=None, out=None, stream=None):
     """Give pages back: all pages of rows with release[row] true (their length
     becomes 0), and of the others those that no query of `attend_window_paged`
-    with this window and sinks sees any more (window None: none of them).
+    with this window and sinks sees any more (window None: none of them; 0: a
+    window of no positions, every whole page behind the sinks).
 
     block_tables [rows, max_blocks], context_lens [rows], refs [num_blocks]
     int32; release [rows] bool or uint8, or None. Returns new (block_tables,
@@ -613,7 +620,8 @@ class TQPagePools:
         """Make row children[i] a copy of row parents[i]: the parent's full
         pages are shared, a partly filled last page is copied to the lowest
         free page. parents, children [n] int32; other tensors as `pages_trim`.
-        A child's former pages are not given back (`pages_trim` first). Returns
+        A child's former pages are not given back (`pages_trim` first). No
+        tensor shares memory with a pool, `workspace` with none at all. Returns
         (block_tables, context_lens, refs)."""
         args = (*self._mine, block_tables, context_lens, refs, parents, children, out, workspace)
         if stream is not None:

@@ -47,9 +47,10 @@
 // Bound: (P_K + P_V + 8) bytes per visible position and kv head, against about
 // 680 warp instructions and 200 shared-memory wavefronts per 32 positions and
 // kv head. Measured, 16 sequences with 8192 visible positions, 32 query and 8 kv
-// heads of 128, keys 4 and values 2 bits (109 MB): 45 us (2.4 TB/s) and 7 us
-// of merge alone, 47.6 us together; issue slots 55 %, shared-memory pipe 60 %,
-// ALU 47 %. More warps of fewer registers (24 of 80) take 55 us: the pipes are
+// heads of 128, keys 4 and values 2 bits (109 MB): 48.2 us a call (2.3 TB/s;
+// each kernel by itself 45 and its merge 7, which overlap); issue slots 55 %,
+// shared-memory pipe 59 %, ALU 47 %. The instances at 128 registers spill a few words
+// (head_dim 128, up to 4 query rows). More warps of fewer registers (24 of 80) take 55 us: the pipes are
 // what is shared, not latency that is left open.
 #include <climits>
 #include <cmath>
@@ -180,8 +181,8 @@ __global__ void __launch_bounds__(AwCfg<D, KB, VB, NT>::WARPS * 32, 1)
   constexpr int NB = D / 16;
   constexpr int RT = 4 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
-  // what is the same for a warp is broadcast from its first lane: the compiler
-  // then keeps what follows from it (blocks, addresses) in uniform registers
+  // what is the same for a warp is broadcast from its first lane, so that what
+  // follows from it (blocks, addresses) is known to be the same for the warp
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int gq = lane >> 2, tq = lane & 3;
   const int b = blockIdx.z;
@@ -666,8 +667,8 @@ __global__ void __launch_bounds__(AwCfg<D, KB, VB, NT>::WARPS * 32, 1)
 // Merge of the splits of a row, one warp per row: M = max m_s, weights
 // 2^(m_s - M), o = D_V H_pm (sum_s weight acc_s / sum_s weight l_s) / d.
 // (Starting it while the partial kernel's last CTAs still run, by an early
-// griddepcontrol.launch_dependents there, costs: 16 x 8192 positions 49.0 ->
-// 51.3 us, 8 x 5 tokens 61.5 -> 63.0.)
+// griddepcontrol.launch_dependents there, cost when it was tried: 16 x 8192
+// positions 49.0 -> 51.3 us, 8 x 5 tokens 61.5 -> 63.0.)
 template <int D>
 __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_constant__ AwArgs a) {
   constexpr int E = D / 32;  // elements of a lane: dims [E lane, + E)
@@ -749,7 +750,13 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_consta
 // kv head, the tensor-memory kernel the same up to 128 (d = 256) or 256 rows,
 // but more to start; so that one takes 64 rows and more, this one fewer than 40
 // (32 at d = 256), and between them the estimates below decide (us; `seen`
-// positions at most). Measured, this kernel / that one, keys 4 and values 2 bits:
+// positions at most). They were fitted to, and checked at, sizes in that range
+// only, so they stop at 64 rows, although one short sequence loses there: 64 rows over
+// 300 positions take about 15 us on this kernel and 22.7 on that one. `rows` is
+// that of the longest sequence: one kernel and one number of splits serve all of
+// a call (32 sequences over 8192 positions, a chunk of 2048 tokens in one and a
+// token in each other: 965 us, the chunk alone 491, the 31 tokens alone 111).
+// Measured, this kernel / that one, keys 4 and values 2 bits:
 //   d = 128, 8 sequences x 4 kv heads x 8000: 32 rows 56 / 62, 40 rows 68 / 63, 64 rows 105 / 63
 //            32 x 8 x 1000: 40 rows 60 / 81, 48 rows 97 / 81;  32 x 8 x 2000: 106 / 122, 169 / 123
 //            8 x 8 x 2000: 40 rows 46 / 39;  1 x 8 x 300: 48 rows 15 / 23;  1 x 8 x 1000: 48 rows 18 / 25

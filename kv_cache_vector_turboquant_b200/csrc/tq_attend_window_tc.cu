@@ -42,15 +42,16 @@
 // 9 other instructions per score and the codes' conversion (about 1000 warp
 // instructions, shared by the row tiles). Measured, 2 x 2048 tokens of 32 query
 // and 8 kv heads of 128 within 4096 + 64 positions, keys 4 and values 2 bits:
-// 616 us a call, 0.90 PFLOP/s with the remainders counted. A CTA's loop takes
+// 614 to 632 us a call on different GPUs (945 k cycles), 0.89 PFLOP/s with the
+// remainders counted. A CTA's loop takes
 // about 3700 cycles per 64 positions, of which a softmax warp works 3300 (some
 // 550 instructions at 6 cycles each: 20 warps, a fifth of the wait for
 // instructions; issue slots 54 %, tensor pipe 50 %), so the softmax of a row
 // tile is the bound, not the products; its start took 12 000 to 16 000 cycles
 // (8 000 to 12 000 of them the rotation of the query rows, before it ran in
-// packed additions: 626 -> 616 us, and 66 -> 61.5 below) and its end 9 000; 512
+// packed additions: 626 -> 616 us then, and 66 -> 61.5 below) and its end 9 000; 512
 // CTAs leave 148 SMs 3.46 waves. 8 x 5 tokens of 8 query heads per kv head over
-// 8000 positions, 4 bits: 61.5 us (two softmax groups and the value conversion,
+// 8000 positions, 4 bits: 63.5 us (two softmax groups and the value conversion,
 // 2000 cycles a tile, both take about 4000 cycles per two tiles). Loading codes
 // one more tile ahead changes nothing.
 #include <climits>

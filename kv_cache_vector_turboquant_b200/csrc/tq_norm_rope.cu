@@ -15,7 +15,7 @@
 //
 // Bound: 2 B read and 2 B written per coordinate. Measured, 8191 tokens of 40
 // heads of 128 bf16 coordinates with norm and 64 of them rotated (168 MB):
-// 36.9 us, 4.5 TB/s (25.5 us at a plain copy's rate); the schedulers issue 78 %
+// 36.7 us, 4.6 TB/s (25.5 us at a plain copy's rate); the schedulers issue 78 %
 // of their slots, about 154 warp instructions per pass (two rows of 128), so
 // instructions are the bound there. 16 tokens take 4.2 us, a launch's latency
 // and the chain position -> angle -> row.
