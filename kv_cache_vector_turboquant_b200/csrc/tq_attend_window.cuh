@@ -145,11 +145,12 @@ TQ_DEV float aw_pow2_for(float mag, float& inv) {
 // then lie below AW_SMALL, where its fp16 remainder (a multiple of 2^-24) runs
 // out of bits: norms that this row does not see, or positions that it gives no
 // weight, may be larger by any factor. Then the reference is lowered until that
-// product lies in [2^2, 2^3), or the row's sum of weights near 2^AW_SUM. (With 2
+// product lies in [2^2, 2^3), or the row's sum of weights near 2^AW_SUM (so that
+// norms 2^90 apart are covered over 2^24 positions of one weight). (With 2
 // for AW_SMALL and [2^5, 2^6), 2 x 2048 tokens whose norms spread by e^1 took
 // 1018 us, with these 734, both before tw_largest took logarithms.)
 constexpr float AW_SMALL = 0.25f;
-constexpr int AW_SUM = 100;
+constexpr int AW_SUM = 110;
 // Reference for a row whose scores have reached `top`, at which its sum is `sum`
 // and its largest weight x norm `most`, which becomes the one at the result.
 TQ_DEV float aw_reference(float top, float sum, float& most) {

@@ -42,7 +42,7 @@
 // 9 other instructions per score and the codes' conversion (about 1000 warp
 // instructions, shared by the row tiles). Measured, 2 x 2048 tokens of 32 query
 // and 8 kv heads of 128 within 4096 + 64 positions, keys 4 and values 2 bits:
-// 614 to 632 us a call on different GPUs (945 k cycles), 0.89 PFLOP/s with the
+// 614 to 635 us a call on different GPUs (945 k cycles), 0.89 PFLOP/s with the
 // remainders counted. A CTA's loop takes
 // about 3700 cycles per 64 positions, of which a softmax warp works 3300 (some
 // 550 instructions at 6 cycles each: 20 warps, a fifth of the wait for
